@@ -31,7 +31,8 @@ LINK_FLAGS = ARCH_FLAGS + ["--shared", "-cudart", "static", "-Xcompiler", "-fvis
 # Translation units: the host side (validation, launch planning, C ABI) and
 # one unit per kernel family, compiled in parallel.
 UNITS = ["hadq_api.cu", "kernels_segment.cu", "kernels_team.cu", "kernels_team_bf16.cu", "kernels_tc.cu",
-         "kernels_tck.cu", "kernels_ksize.cu", "kernels_ksize_bf16.cu", "hadq_codebook.cu"]
+         "kernels_tck.cu", "kernels_ksize.cu", "kernels_ksize_bf16.cu", "hadq_codebook.cu", "hadq_layer_api.cu",
+         "kernels_norm.cu", "kernels_imm.cu", "kernels_kv4.cu"]
 
 
 def _nvcc() -> str:

@@ -5,11 +5,10 @@
 // rule the apply_spinquant docstring states for its rotation passes).  There
 // is no CPU path: a missing device or kernel image surfaces as HADQ_ERR_CUDA.
 #include "hadq.h"
+#include "hadq_host.h"
 #include "hadq_kernels.cuh"   // launch constants only; the kernels are instantiated elsewhere
 #include "hadq_ksize.cuh"
 #include "hadq_launch.h"
-
-#include <cudaTypedefs.h>
 
 #include <atomic>
 
@@ -24,13 +23,103 @@
 #include <tuple>
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace hadq {
+namespace host {
 
 hadq_status fail(hadq_status st, const std::string& msg) {
   g_last_error = msg;
   return st;
 }
+
+void clear_error() { g_last_error.clear(); }
+
+}  // namespace host
+}  // namespace hadq
+
+// ------------------------------------------------- per-device launch caches
+
+namespace {
+std::mutex g_mu;
+std::map<int, int> g_sms;                                    // device -> SM count
+std::map<std::tuple<int, const void*, int, int>, int> g_occ; // (device, fn, block, smem) -> CTAs/SM
+std::map<std::pair<int, const void*>, int> g_smem_limit;   // (device, fn) -> dynamic smem limit set
+}  // namespace
+
+namespace hadq {
+namespace host {
+
+hadq_status device_sms(int* sms, int* dev_out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_sms.find(dev);
+  if (it == g_sms.end()) {
+    int v = 0;
+    e = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("cudaDeviceGetAttribute: ") + cudaGetErrorString(e));
+    it = g_sms.emplace(dev, v).first;
+  }
+  *sms = it->second;
+  *dev_out = dev;
+  return HADQ_OK;
+}
+
+hadq_status occupancy(const void* fn, int dev, int block, int smem, int* occ) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  const auto key = std::make_tuple(dev, fn, block, smem);
+  auto it = g_occ.find(key);
+  if (it == g_occ.end()) {
+    cudaError_t e = cudaSuccess;
+    int& limit = g_smem_limit[std::make_pair(dev, fn)];
+    if (smem > limit) {
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+      limit = smem;
+    }
+    int v = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, block, smem);
+    if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("occupancy query: ") + cudaGetErrorString(e));
+    if (v < 1) return fail(HADQ_ERR_CUDA, "kernel does not fit on an SM");
+    it = g_occ.emplace(key, v).first;
+  }
+  *occ = it->second;
+  return HADQ_OK;
+}
+
+hadq_status check_launch(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return HADQ_OK;
+}
+
+hadq_status launch_result(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return check_launch(what);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+}  // namespace host
+}  // namespace hadq
+
+namespace {
+
+using namespace hadq::host;
 
 bool is_pow2(int64_t v) { return v >= 1 && (v & (v - 1)) == 0; }
 
@@ -39,21 +128,6 @@ int ilog2(int64_t v) {
   while ((int64_t(1) << k) < v) ++k;
   return k;
 }
-
-int64_t esize(hadq_dtype d) { return d == HADQ_F32 ? 4 : 2; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;
-};
-
-Span span(const void* p, int64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 constexpr int kMaxBlock = 8192;
 constexpr int64_t kMaxInt8N = 32768;
@@ -190,88 +264,6 @@ int64_t scales_bytes(int64_t rows, int64_t n, hadq_fmt fmt, int group) {
 using hadq::Signs;
 namespace hl = hadq::launch;
 
-// ------------------------------------------------- per-device launch caches
-
-std::mutex g_mu;
-std::map<int, int> g_sms;                                    // device -> SM count
-std::map<std::tuple<int, const void*, int, int>, int> g_occ; // (device, fn, block, smem) -> CTAs/SM
-
-hadq_status device_sms(int* sms, int* dev_out) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
-  std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_sms.find(dev);
-  if (it == g_sms.end()) {
-    int v = 0;
-    e = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("cudaDeviceGetAttribute: ") + cudaGetErrorString(e));
-    it = g_sms.emplace(dev, v).first;
-  }
-  *sms = it->second;
-  *dev_out = dev;
-  return HADQ_OK;
-}
-
-// Resident CTAs per SM for `fn` at this block/smem size.  Also raises the
-// dynamic shared memory limit of `fn` on this device when it needs more than
-// 48 KB; the limit only ever grows (a kernel whose shared memory depends on
-// the call must keep the largest size any earlier call of it needed).
-std::map<std::pair<int, const void*>, int> g_smem_limit;   // (device, fn) -> dynamic smem limit set
-
-hadq_status occupancy(const void* fn, int dev, int block, int smem, int* occ) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  const auto key = std::make_tuple(dev, fn, block, smem);
-  auto it = g_occ.find(key);
-  if (it == g_occ.end()) {
-    cudaError_t e = cudaSuccess;
-    int& limit = g_smem_limit[std::make_pair(dev, fn)];
-    if (smem > limit) {
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
-      limit = smem;
-    }
-    int v = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, fn, block, smem);
-    if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string("occupancy query: ") + cudaGetErrorString(e));
-    if (v < 1) return fail(HADQ_ERR_CUDA, "kernel does not fit on an SM");
-    it = g_occ.emplace(key, v).first;
-  }
-  *occ = it->second;
-  return HADQ_OK;
-}
-
-hadq_status check_launch(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-  return HADQ_OK;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Launch with programmatic stream serialization: the kernel may be scheduled
-// while the previous kernel in the stream drains; it waits for that kernel's
-// completion (griddepcontrol.wait) before touching global memory.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*fn)(KArgs...), int64_t grid, int block, int smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(block));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
-}
-
-hadq_status launch_result(cudaError_t e, const char* what) {
-  if (e != cudaSuccess) return fail(HADQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-  return check_launch(what);
-}
-
 // ------------------------------------------------------- tensor-core path
 
 // Which implementation serves the calls both implementations cover (bf16
@@ -281,19 +273,6 @@ std::atomic<int> g_impl{HADQ_IMPL_AUTO};
 
 bool tc_eligible(hadq_dtype x_dtype, const Shape& sh, int mode) {
   return x_dtype == HADQ_BF16 && sh.kbase == 1 && (sh.logb == 12 || sh.logb == 13) && mode >= 0;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
 }
 
 // Blocks of b = 2^(7 + LO) bf16 elements, each rotated in full: the blocks are
@@ -1006,7 +985,8 @@ hadq_impl hadq_get_impl(void) { return static_cast<hadq_impl>(g_impl.load(std::m
 
 int hadq_device_faults(int clear) {
   const int a = hadq::launch::tc_fault_bits(clear), b = hadq::launch::tck_fault_bits(clear);
-  return a < 0 || b < 0 ? -1 : (a | b);
+  const int c = hadq::launch::kv4_fault_bits(clear);
+  return a < 0 || b < 0 || c < 0 ? -1 : (a | b | c);
 }
 
 }  // extern "C"

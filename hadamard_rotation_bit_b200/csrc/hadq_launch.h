@@ -27,6 +27,13 @@ using Tc128Fn = void (*)(const CUtensorMap, const CUtensorMap, const uint16_t*, 
 namespace ksize {
 struct StageArgs;
 }
+namespace kv4 {
+struct AppendArgs;
+struct AttnArgs;
+}
+namespace imm {
+struct Args;
+}
 namespace launch {
 using KsFn = void (*)(const ksize::StageArgs);
 
@@ -87,6 +94,32 @@ KsFn staged_kernel_bf16(int k, int shi, int mode, int sgk);
 // K * hi <= 128 chunks of 128); mode OUT_F32 / OUT_BF16, -1 = per-token int8
 // (block = row), or OUT_INT4 / OUT_MXFP4 / OUT_NVFP4.
 TckVariant tck_kernel_for(int k, int hi, int mode);
+
+// Norm kernels: rows per CTA and threads of the variant for a row length.
+using NormFn = void (*)(const void*, const void*, const void*, int64_t, int, float, void*, int8_t*, float*);
+struct NormVariant {
+  NormFn fn;
+  int threads, rows_per_cta;
+};
+NormVariant norm_kernel_for(bool bf16, bool residual, int64_t rows, int64_t n);
+
+// int8 matrix product.
+using ImmFn = void (*)(const imm::Args);
+ImmFn imm_plain_for(bool out_bf16);
+
+// int4 cache: append, attention (rows = query rows per K/V head; the variant
+// takes `rows` of them per CTA) and the join of its splits.
+using AppendFn = void (*)(const kv4::AppendArgs);
+using AttnFn = void (*)(const kv4::AttnArgs);
+using JoinFn = void (*)(const float*, const float2*, int64_t, int, uint16_t*);
+struct AttnVariant {
+  AttnFn fn;
+  int threads, smem, rows;
+};
+AppendFn kv4_append_for(bool bf16, int d);
+AttnVariant kv4_attention_for(int d, int group, int rows);
+JoinFn kv4_join_for(int d);
+int kv4_fault_bits(int clear);
 
 // The tensor-core kernels' sticky fault words (bounded waits that ran out),
 // one per translation unit; cleared when `clear` is non-zero.  -1 on a CUDA

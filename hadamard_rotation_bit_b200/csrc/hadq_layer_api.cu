@@ -1,0 +1,337 @@
+// Host side of the operators around the rotation: the int8 norm and matrix
+// product, and the int4 cache.  As everywhere in the library every check runs
+// before the first CUDA call, and nothing is allocated.
+#include "hadq_host.h"
+#include "hadq_imm.cuh"
+#include "hadq_kv4.cuh"
+#include "hadq_launch.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <string>
+
+namespace {
+
+using namespace hadq::host;
+namespace hl = hadq::launch;
+
+// No exception leaves a C entry point (host memory can run out in a message
+// or a launch cache).
+template <typename F>
+hadq_status entry(F&& body) {
+  try {
+    clear_error();
+    return body();
+  } catch (...) {
+    return HADQ_ERR_CUDA;
+  }
+}
+
+hadq_status invalid(const char* msg) { return fail(HADQ_ERR_INVALID_ARG, msg); }
+hadq_status unsupported(const char* msg) { return fail(HADQ_ERR_UNSUPPORTED, msg); }
+
+bool dtype_ok(hadq_dtype d) { return d == HADQ_F32 || d == HADQ_BF16; }
+
+// Outputs must not overlap an input or one another.
+hadq_status disjoint(const Span* outs, int nouts, const Span* ins, int nins, const char* msg) {
+  for (int i = 0; i < nouts; ++i) {
+    for (int j = 0; j < nins; ++j)
+      if (overlaps(outs[i], ins[j])) return invalid(msg);
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outs[j])) return invalid(msg);
+  }
+  return HADQ_OK;
+}
+
+constexpr int64_t kMaxNormN = 32768;
+constexpr int64_t kMaxK = 131071;        // 128 * 128 * k < 2^31
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+constexpr int64_t kMaxGridY = 65535;
+
+// What the two cache entry points share.
+struct Cache {
+  int64_t kv_heads, head_dim, group, num_pages, page_size;
+  const void *k_codes, *k_scales, *v_codes, *v_scales;
+};
+
+hadq_status check_cache_shape(const Cache& c) {
+  if (c.kv_heads <= 0 || c.num_pages <= 0 || c.page_size <= 0) return invalid("kv_heads, num_pages and page_size must be > 0");
+  if (c.group != 32 && c.group != 64 && c.group != 128) return invalid("int4 group must be 32, 64 or 128");
+  if (c.head_dim != 64 && c.head_dim != 128) return unsupported("head_dim must be 64 or 128");
+  if (c.head_dim % c.group != 0) return invalid("int4 group must divide head_dim");
+  if (c.page_size % 16 != 0) return unsupported("page_size must be a multiple of 16");
+  if (c.page_size > kMaxDim || c.num_pages > kMaxDim || c.num_pages * c.page_size > INT32_MAX)
+    return unsupported("the cache must hold fewer than 2^31 positions");
+  if (c.kv_heads > 65536) return unsupported("at most 65536 K/V heads");
+  return HADQ_OK;
+}
+
+hadq_status check_cache_pointers(const Cache& c, Span (&spans)[4]) {
+  if (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales) return invalid("null pointer");
+  if (!aligned16(c.k_codes) || !aligned16(c.k_scales) || !aligned16(c.v_codes) || !aligned16(c.v_scales))
+    return fail(HADQ_ERR_MISALIGNED, "the cache's pointers must be 16-byte aligned");
+  const int64_t cells = c.num_pages * c.page_size * c.kv_heads;
+  const int64_t cb = cells * (c.head_dim / 2), sb = cells * (c.head_dim / c.group) * 2;
+  spans[0] = span(c.k_codes, cb);
+  spans[1] = span(c.k_scales, sb);
+  spans[2] = span(c.v_codes, cb);
+  spans[3] = span(c.v_scales, sb);
+  return disjoint(spans, 4, nullptr, 0, "the cache's four tensors must not overlap");
+}
+
+// block: the whole head, or 1 (H_1: none).
+hadq_status check_block(int64_t block, int64_t head_dim, int* rotate) {
+  if (block == 0 || block == -1 || block == head_dim) *rotate = 1;
+  else if (block == 1) *rotate = 0;
+  else return unsupported("block must be 0 or head_dim (each head rotated in full) or 1 (no rotation)");
+  return HADQ_OK;
+}
+
+// Splits of a sequence over CTAs.  Rule (sizes only, so that a captured call
+// and its workspace hold for any lengths): enough CTAs to fill 148 SMs with 4
+// each, and at least 8 tiles of 16 positions for a CTA's 4 warps.
+int kv4_splits(int64_t units, int64_t capacity) {
+  const int64_t want = ceil_div(148 * 4, std::max<int64_t>(units, 1));
+  const int64_t most = std::max<int64_t>(1, capacity / 128);
+  return static_cast<int>(std::min<int64_t>(std::min(want, most), 256));
+}
+
+int64_t kv4_row_tiles(int64_t rows) { return rows <= 8 ? 1 : ceil_div(rows, 16); }
+
+hadq_status check_attention_shape(int64_t batch, int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  int64_t max_positions) {
+  if (batch < 0) return invalid("batch must be >= 0");
+  if (q_len < 1 || heads < 1 || kv_heads < 1) return invalid("q_len, heads and kv_heads must be > 0");
+  if (heads % kv_heads != 0) return invalid("heads must be a multiple of kv_heads");
+  if (head_dim != 64 && head_dim != 128) return unsupported("head_dim must be 64 or 128");
+  if (q_len > 64) return unsupported("q_len above 64: this call is for the newest tokens of a sequence");
+  if (heads > 65536 || batch > kMaxDim) return unsupported("batch or heads too large");
+  if (max_positions < 1) return invalid("max_pages must be > 0");
+  if (max_positions > kMaxDim) return unsupported("sequences of more than 2^30 positions");
+  if (batch * kv_heads * kv4_row_tiles(q_len * (heads / kv_heads)) > INT32_MAX) return unsupported("batch * heads too large");
+  return HADQ_OK;
+}
+
+int64_t attention_workspace(int64_t batch, int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                            int64_t max_positions, int* splits) {
+  *splits = kv4_splits(batch * kv_heads * kv4_row_tiles(q_len * (heads / kv_heads)), max_positions);
+  return *splits == 1 ? 0 : *splits * batch * q_len * heads * (head_dim + 2) * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+hadq_status hadq_rmsnorm_quant(const void* x, hadq_dtype x_dtype, int64_t rows, int64_t n, const void* residual,
+                               const void* weight, float eps, void* residual_out, int8_t* codes, float* scales,
+                               void* stream) {
+  return entry([&]() -> hadq_status {
+    if (!dtype_ok(x_dtype)) return invalid("x_dtype must be HADQ_F32 or HADQ_BF16");
+    if (rows < 0) return invalid("rows must be >= 0");
+    if (n <= 0) return invalid("n must be > 0");
+    if (!(std::isfinite(eps) && eps >= 0.f)) return invalid("eps must be finite and >= 0");
+    if (n % 8 != 0) return unsupported("n must be a multiple of 8");
+    if (n > kMaxNormN) return unsupported("the norm supports n <= 32768");
+    if (rows > INT64_MAX / 8 / n) return invalid("rows * n overflows");
+    if ((residual == nullptr) != (residual_out == nullptr) && rows > 0)
+      return invalid("residual and residual_out are given together or not at all");
+    if (rows == 0) return HADQ_OK;
+    if (!x || !weight || !codes || !scales) return invalid("null pointer");
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(codes) || !aligned16(scales) || !aligned16(residual) ||
+        !aligned16(residual_out))
+      return fail(HADQ_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    const int64_t bytes = rows * n * esize(x_dtype);
+    const Span outs[3] = {span(codes, rows * n), span(scales, rows * 4), span(residual_out, residual ? bytes : 0)};
+    const Span ins[3] = {span(x, bytes), span(weight, n * esize(x_dtype)), span(residual, residual ? bytes : 0)};
+    hadq_status st = disjoint(outs, 2, ins, 3, "codes and scales must not overlap an input or each other");
+    if (st != HADQ_OK) return st;
+    if (residual) {
+      for (int i = 0; i < 3; ++i)
+        if (overlaps(outs[2], ins[i]) && !(i != 1 && outs[2].lo == ins[i].lo))
+          return invalid("residual_out may be x or residual, and must not overlap an input otherwise");
+      if (overlaps(outs[2], outs[0]) || overlaps(outs[2], outs[1])) return invalid("outputs must not overlap");
+    }
+    const hl::NormVariant v = hl::norm_kernel_for(x_dtype == HADQ_BF16, residual != nullptr, rows, n);
+    const int64_t grid = ceil_div(rows, v.rows_per_cta);
+    if (grid > INT32_MAX) return unsupported("too many rows");
+    return launch_result(launch_pdl(v.fn, grid, v.threads, 0, static_cast<cudaStream_t>(stream), x, residual, weight,
+                                    rows, static_cast<int>(n), eps, residual_out, codes, scales),
+                         "norm kernel launch");
+  });
+}
+
+hadq_status hadq_matmul_int8(const int8_t* a, const float* a_scales, int64_t rows, const int8_t* w,
+                             const float* w_scales, int64_t cols, int64_t k, const float* bias, void* out,
+                             hadq_dtype out_dtype, void* stream) {
+  return entry([&]() -> hadq_status {
+    if (!dtype_ok(out_dtype)) return invalid("out_dtype must be HADQ_F32 or HADQ_BF16");
+    if (rows < 0 || cols < 0) return invalid("rows and cols must be >= 0");
+    if (k <= 0) return invalid("k must be > 0");
+    if (k % 16 != 0) return unsupported("k must be a multiple of 16");
+    if (k > kMaxK) return unsupported("k above 131071 could leave 32-bit sums");
+    if (rows > kMaxDim || cols > kMaxDim) return unsupported("rows and cols must be at most 2^30");
+    if (rows == 0 || cols == 0) return HADQ_OK;
+    if (!a || !a_scales || !w || !w_scales || !out) return invalid("null pointer");
+    if (!aligned16(a) || !aligned16(a_scales) || !aligned16(w) || !aligned16(w_scales) || !aligned16(bias) ||
+        !aligned16(out))
+      return fail(HADQ_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    const Span o = span(out, rows * cols * esize(out_dtype));
+    const Span ins[5] = {span(a, rows * k), span(a_scales, rows * 4), span(w, cols * k), span(w_scales, cols * 4),
+                         span(bias, bias ? cols * 4 : 0)};
+    hadq_status st = disjoint(&o, 1, ins, 5, "out must not overlap an input");
+    if (st != HADQ_OK) return st;
+    const hadq::imm::Args p{a, w, a_scales, w_scales, bias, out, static_cast<int>(rows), static_cast<int>(cols),
+                            static_cast<int>(k)};
+    const dim3 grid(static_cast<unsigned>(ceil_div(cols, 64)), static_cast<unsigned>(ceil_div(rows, 64)));
+    return launch_result(launch_pdl3(hl::imm_plain_for(out_dtype == HADQ_BF16), grid, 1, 256, 0,
+                                     static_cast<cudaStream_t>(stream), p),
+                         "int8 matrix product launch");
+  });
+}
+
+hadq_status hadq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, hadq_dtype dtype,
+                            int64_t tokens, int64_t kv_heads, int64_t head_dim, int64_t block, int64_t group,
+                            const int64_t* slots, int64_t num_pages, int64_t page_size, void* k_codes, void* k_scales,
+                            void* v_codes, void* v_scales, void* stream) {
+  return entry([&]() -> hadq_status {
+    if (!dtype_ok(dtype)) return invalid("dtype must be HADQ_F32 or HADQ_BF16");
+    if (tokens < 0) return invalid("tokens must be >= 0");
+    const Cache c{kv_heads, head_dim, group, num_pages, page_size, k_codes, k_scales, v_codes, v_scales};
+    hadq_status st = check_cache_shape(c);
+    if (st != HADQ_OK) return st;
+    int rotate = 0;
+    st = check_block(block, head_dim, &rotate);
+    if (st != HADQ_OK) return st;
+    const int64_t width = kv_heads * head_dim, unit = 16 / esize(dtype);
+    if (k_stride < width || v_stride < width) return invalid("k_stride and v_stride must be at least kv_heads * head_dim");
+    if (k_stride % unit != 0 || v_stride % unit != 0) return fail(HADQ_ERR_MISALIGNED, "k_stride and v_stride must be multiples of 16 bytes");
+    if (tokens > kMaxDim || k_stride > kMaxDim || v_stride > kMaxDim) return unsupported("tokens and strides must be at most 2^30");
+    if (tokens == 0) return HADQ_OK;
+    if (!k || !v || !slots) return invalid("null pointer");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return fail(HADQ_ERR_MISALIGNED, "k, v and slots must be 16-byte aligned");
+    Span outs[4];
+    st = check_cache_pointers(c, outs);
+    if (st != HADQ_OK) return st;
+    const int64_t es = esize(dtype);
+    const Span ins[3] = {span(k, ((tokens - 1) * k_stride + width) * es), span(v, ((tokens - 1) * v_stride + width) * es),
+                         span(slots, tokens * 8)};
+    st = disjoint(outs, 4, ins, 3, "the cache must not overlap k, v or slots");
+    if (st != HADQ_OK) return st;
+    hadq::kv4::AppendArgs p;
+    p.x[0] = k, p.x[1] = v;
+    p.stride[0] = k_stride, p.stride[1] = v_stride;
+    p.codes[0] = static_cast<uint8_t*>(k_codes), p.codes[1] = static_cast<uint8_t*>(v_codes);
+    p.scales[0] = static_cast<__half*>(k_scales), p.scales[1] = static_cast<__half*>(v_scales);
+    p.slots = slots;
+    p.tokens = tokens;
+    p.num_slots = num_pages * page_size;
+    p.kv_heads = static_cast<int>(kv_heads);
+    p.page_size = static_cast<int>(page_size);
+    p.group = static_cast<int>(group);
+    p.rotate_k = rotate;
+    p.norm = static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
+    const int64_t grid = ceil_div(tokens * kv_heads * (head_dim / 32), 256);
+    if (grid > INT32_MAX) return unsupported("too many rows");
+    return launch_result(launch_pdl3(hl::kv4_append_for(dtype == HADQ_BF16, static_cast<int>(head_dim)),
+                                     dim3(static_cast<unsigned>(grid), 2), 1, 256, 0, static_cast<cudaStream_t>(stream), p),
+                         "cache append launch");
+  });
+}
+
+int64_t hadq_kv4_attention_workspace(int64_t batch, int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                     int64_t max_positions) {
+  int64_t bytes = -1;
+  const hadq_status st = entry([&]() -> hadq_status {
+    const hadq_status s = check_attention_shape(batch, q_len, heads, kv_heads, head_dim, max_positions);
+    int splits = 0;
+    if (s == HADQ_OK) bytes = attention_workspace(batch, q_len, heads, kv_heads, head_dim, max_positions, &splits);
+    return s;
+  });
+  return st == HADQ_OK ? bytes : -1;
+}
+
+hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype, int64_t batch, int64_t q_len,
+                               int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t block, int64_t group,
+                               const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                               int64_t num_pages, int64_t page_size, const int32_t* page_table, int64_t max_pages,
+                               const int32_t* lengths, float scale, void* out, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+  return entry([&]() -> hadq_status {
+    if (!dtype_ok(dtype)) return invalid("dtype must be HADQ_F32 or HADQ_BF16");
+    if (dtype != HADQ_BF16) return unsupported("attention takes bf16 queries");
+    const Cache c{kv_heads, head_dim, group, num_pages, page_size, k_codes, k_scales, v_codes, v_scales};
+    hadq_status st = check_cache_shape(c);
+    if (st != HADQ_OK) return st;
+    if (max_pages < 1 || max_pages > kMaxDim) return invalid("max_pages must be > 0");
+    st = check_attention_shape(batch, q_len, heads, kv_heads, head_dim, max_pages * page_size);
+    if (st != HADQ_OK) return st;
+    int rotate = 0;
+    st = check_block(block, head_dim, &rotate);
+    if (st != HADQ_OK) return st;
+    if (!std::isfinite(scale)) return invalid("scale must be finite");
+    if (q_stride < heads * head_dim) return invalid("q_stride must be at least heads * head_dim");
+    if (q_stride % 8 != 0) return fail(HADQ_ERR_MISALIGNED, "q_stride must be a multiple of 16 bytes");
+    if (q_stride > kMaxDim) return unsupported("q_stride must be at most 2^30");
+    if (batch == 0) return HADQ_OK;
+    if (!q || !page_table || !lengths || !out) return invalid("null pointer");
+    if (!aligned16(q) || !aligned16(page_table) || !aligned16(lengths) || !aligned16(out) || !aligned16(workspace))
+      return fail(HADQ_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    Span cache[4];
+    st = check_cache_pointers(c, cache);
+    if (st != HADQ_OK) return st;
+    int splits = 0;
+    const int64_t need = attention_workspace(batch, q_len, heads, kv_heads, head_dim, max_pages * page_size, &splits);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+      return invalid("workspace is smaller than hadq_kv4_attention_workspace says");
+    const int64_t out_rows = batch * q_len * heads;
+    const Span outs[2] = {span(out, out_rows * head_dim * 2), span(workspace, need)};
+    const Span ins[7] = {span(q, ((batch * q_len - 1) * q_stride + heads * head_dim) * 2), span(page_table, batch * max_pages * 4),
+                         span(lengths, batch * 4), cache[0], cache[1], cache[2], cache[3]};
+    st = disjoint(outs, need > 0 ? 2 : 1, ins, 7, "out and workspace must not overlap an input or each other");
+    if (st != HADQ_OK) return st;
+    const int ratio = static_cast<int>(heads / kv_heads);
+    const int64_t rows = q_len * ratio, row_tiles = kv4_row_tiles(rows);
+    const hl::AttnVariant v = hl::kv4_attention_for(static_cast<int>(head_dim), static_cast<int>(group), static_cast<int>(rows));
+    if (v.fn == nullptr) return unsupported("no attention kernel for this head_dim and group");
+    hadq::kv4::AttnArgs p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride = q_stride;
+    p.k_codes = static_cast<const uint8_t*>(k_codes);
+    p.k_scales = static_cast<const __half*>(k_scales);
+    p.v_codes = static_cast<const uint8_t*>(v_codes);
+    p.v_scales = static_cast<const __half*>(v_scales);
+    p.table = page_table;
+    p.lengths = lengths;
+    p.out = static_cast<uint16_t*>(out);
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + (need > 0 ? splits * out_rows * head_dim : 0));
+    p.num_pages = num_pages;
+    p.out_rows = out_rows;
+    p.max_pages = static_cast<int>(max_pages);
+    p.page_size = static_cast<int>(page_size);
+    p.q_len = static_cast<int>(q_len);
+    p.kv_heads = static_cast<int>(kv_heads);
+    p.ratio = ratio;
+    p.row_tiles = static_cast<int>(row_tiles);
+    p.splits = splits;
+    p.rotate = rotate;
+    p.norm = static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    int sms = 0, dev = 0, occ = 0;
+    st = device_sms(&sms, &dev);
+    if (st != HADQ_OK) return st;
+    st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
+    if (st != HADQ_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(batch * kv_heads * row_tiles), static_cast<unsigned>(splits)),
+                                   1, v.threads, v.smem, s, p),
+                       "cache attention launch");
+    if (st != HADQ_OK || splits == 1) return st;
+    return launch_result(launch_pdl(hl::kv4_join_for(static_cast<int>(head_dim)), ceil_div(out_rows, 4), 128, 0, s,
+                                    const_cast<const float*>(p.part_o), const_cast<const float2*>(p.part_ml), out_rows, splits, p.out),
+                         "cache attention join launch");
+  });
+}
+
+}  // extern "C"

@@ -32,6 +32,8 @@ EXPORTS = (
     "hadq_device_faults", "hadq_rotate_quant_host_static", "hadq_rotate_signed", "hadq_rotate_quant_signed",
     "hadq_rotate_quant_nvfp4", "hadq_set_impl", "hadq_get_impl", "hadq_codebook",
     "hadq_rotate_rpbh", "hadq_rotate_quant_rpbh", "hadq_rotate_quant_codebook",
+    "hadq_rmsnorm_quant", "hadq_matmul_int8", "hadq_kv4_append", "hadq_kv4_attention",
+    "hadq_kv4_attention_workspace",
 )
 IMPLS = {"auto": 0, "butterfly": 1, "tensor": 2}
 
@@ -93,6 +95,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.hadq_rotate_quant_rpbh.restype = i32
         lib.hadq_rotate_quant_codebook.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, vp, vp, vp, vp]
         lib.hadq_rotate_quant_codebook.restype = i32
+        f32 = ctypes.c_float
+        lib.hadq_rmsnorm_quant.argtypes = [vp, i32, i64, i64, vp, vp, f32, vp, vp, vp, vp]
+        lib.hadq_matmul_int8.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, vp, i32, vp]
+        lib.hadq_kv4_append.argtypes = [vp, i64, vp, i64, i32, i64, i64, i64, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp]
+        lib.hadq_kv4_attention.argtypes = [vp, i64, i32, i64, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, i64, i64,
+                                           vp, i64, vp, f32, vp, vp, i64, vp]
+        for f in ("hadq_rmsnorm_quant", "hadq_matmul_int8", "hadq_kv4_append", "hadq_kv4_attention"):
+            getattr(lib, f).restype = i32
+        lib.hadq_kv4_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i64]
+        lib.hadq_kv4_attention_workspace.restype = i64
         _lib = lib
         return lib
 
@@ -439,3 +451,195 @@ def hadq_rotate_quant_codebook(x: torch.Tensor, bits: int, thresholds: torch.Ten
                                           thresholds.data_ptr(), codes.data_ptr(), norms.data_ptr(),
                                           _stream_handle(stream)))
     return codes, norms
+
+
+# ------------------------------------------------- int8 linear and int4 cache
+
+def _invalid(message: str) -> HadqError:
+    return HadqError(HADQ_ERR_INVALID_ARG, message)
+
+
+def _takes(name: str, t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape, contiguous: bool = True) -> int:
+    """Address of a tensor that must have this device, dtype and shape (None: any extent)."""
+    if not t.is_cuda or t.device != dev:
+        _on_device(name, t, dev)
+    if t.dtype != dtype:
+        raise _invalid(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != len(shape) or any(s is not None and s != g for s, g in zip(shape, t.shape)):
+        raise _invalid(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if contiguous and not t.is_contiguous():
+        raise _invalid(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _on:
+    """Device of a call made current for it, and its stream: the one given, or
+    that device's current stream.  Outputs are allocated under it, so a stream
+    given explicitly is the caller's to order with their use, as elsewhere."""
+
+    __slots__ = ("guard", "handle")
+
+    def __init__(self, dev: torch.device, stream):
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self.handle = _stream_handle(torch.cuda.current_stream(dev) if stream is None else stream)
+
+    def __enter__(self) -> int:
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                       residual_out: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                       scales: torch.Tensor | None = None, stream=None):
+    """RMSNorm(x + residual) * weight as int8 codes with a scale per token (see
+    include/hadq.h).  Returns (codes, scales, residual_out); the last is
+    x + residual, or None without a residual.  residual_out may be x or residual."""
+    lib = load_library()
+    rows, n = _rows_n(x)
+    dev = x.device
+    _on_device("x", x, dev)
+    w = _takes("weight", weight, dev, x.dtype, (n,))
+    if residual is not None:
+        _takes("residual", residual, dev, x.dtype, x.shape)
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        _takes("residual_out", residual_out, dev, x.dtype, x.shape)
+    elif residual_out is not None:
+        raise _invalid("residual_out needs a residual")
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    _takes("codes", codes, dev, torch.int8, x.shape)
+    if scales is None:
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _takes("scales", scales, dev, torch.float32, x.shape[:-1])
+    with _on(dev, stream) as s:
+        _check(lib.hadq_rmsnorm_quant(x.data_ptr(), _dtype_code(x.dtype), rows, n,
+                                      None if residual is None else residual.data_ptr(), w, eps,
+                                      None if residual is None else residual_out.data_ptr(), codes.data_ptr(),
+                                      scales.data_ptr(), s))
+    return codes, scales, residual_out
+
+
+def hadq_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                     bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """(a . w^T) * a_scales[:, None] * w_scales + bias of int8 codes a [..., k]
+    and weights w [cols, k] (see include/hadq.h)."""
+    lib = load_library()
+    rows, k = _rows_n(a)
+    dev = a.device
+    _on_device("a", a, dev)
+    ap = _takes("a", a, dev, torch.int8, a.shape)
+    asp = _takes("a_scales", a_scales, dev, torch.float32, a.shape[:-1])
+    wp = _takes("w", w, dev, torch.int8, (None, k))
+    cols = w.shape[0]
+    wsp = _takes("w_scales", w_scales, dev, torch.float32, (cols,))
+    bp = None if bias is None else _takes("bias", bias, dev, torch.float32, (cols,))
+    if out is None:
+        out = torch.empty((*a.shape[:-1], cols), dtype=out_dtype, device=dev)
+    op = _takes("out", out, dev, out.dtype, (*a.shape[:-1], cols))
+    with _on(dev, stream) as s:
+        _check(lib.hadq_matmul_int8(ap, asp, rows, wp, wsp, cols, k, bp, op, _dtype_code(out.dtype), s))
+    return out
+
+
+def _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales):
+    """Addresses and (num_pages, kv_heads, page_size, head_dim, group) of a cache's four tensors."""
+    if k_codes.dim() != 4 or k_scales.dim() != 4:
+        raise _invalid("k_codes and k_scales must be [num_pages, kv_heads, page_size, ...]")
+    pages, heads, size, half = k_codes.shape
+    groups = k_scales.shape[3]
+    if groups == 0 or (2 * half) % groups:
+        raise _invalid(f"{groups} scales for {2 * half} elements")
+    ptrs = [_takes(name, t, dev, dtype, (pages, heads, size, last))
+            for name, t, dtype, last in (("k_codes", k_codes, torch.uint8, half), ("k_scales", k_scales, torch.float16, groups),
+                                         ("v_codes", v_codes, torch.uint8, half), ("v_scales", v_scales, torch.float16, groups))]
+    return ptrs, pages, heads, size, 2 * half, 2 * half // groups
+
+
+def _token_rows(name: str, x: torch.Tensor, tail) -> int:
+    """Elements between the tokens of x [..., heads, head_dim]: heads and their
+    elements dense, tokens (all leading dimensions) evenly spaced."""
+    width = tail[0] * tail[1]
+    if x.stride(-1) != 1 or x.stride(-2) != tail[1]:
+        raise _invalid(f"{name}: the last two dimensions must be dense")
+    stride, step = None, 1
+    for d in range(x.dim() - 3, -1, -1):
+        if x.shape[d] > 1:
+            if stride is None:
+                stride = x.stride(d)
+            elif x.stride(d) != stride * step:
+                raise _invalid(f"{name}: tokens must be evenly spaced")
+        if stride is not None:
+            step *= x.shape[d]
+    return width if stride is None else stride
+
+
+def hadq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
+                    k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor, block: int = 0,
+                    stream=None) -> None:
+    """Rotate (block 0; 1: do not) and quantize the tokens' K, quantize their V,
+    and store both at ``slots`` of the paged int4 cache (see include/hadq.h).
+    k, v: [tokens, kv_heads, head_dim], tokens at any even spacing; slots: int64,
+    negative for tokens that are not stored."""
+    lib = load_library()
+    dev = k.device
+    ptrs, pages, heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
+    kp = _takes("k", k, dev, k.dtype, (None, heads, d), contiguous=False)
+    tokens = k.shape[0]
+    vp = _takes("v", v, dev, k.dtype, (tokens, heads, d), contiguous=False)
+    ks, vs = _token_rows("k", k, (heads, d)), _token_rows("v", v, (heads, d))
+    sp = _takes("slots", slots, dev, torch.int64, (tokens,))
+    with _on(dev, stream) as s:
+        _check(lib.hadq_kv4_append(kp, ks, vp, vs, _dtype_code(k.dtype), tokens, heads, d, block, group, sp, pages, size,
+                                   *ptrs, s))
+
+
+def hadq_kv4_attention_workspace(batch: int, q_len: int, heads: int, kv_heads: int, head_dim: int,
+                                 max_positions: int) -> int:
+    """Bytes of hadq_kv4_attention's workspace (see include/hadq.h)."""
+    n = int(load_library().hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, head_dim, max_positions))
+    if n < 0:
+        raise _invalid(load_library().hadq_last_error().decode())
+    return n
+
+
+def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                       v_scales: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                       scale: float | None = None, block: int = 0, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's newest tokens q [batch, q_len, heads, head_dim]
+    (or [batch, heads, head_dim]) over the paged int4 cache (see include/hadq.h).
+    scale: 1 / sqrt(head_dim) when None.  Without ``workspace`` one is allocated."""
+    lib = load_library()
+    dev = q.device
+    ptrs, pages, kv_heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
+    if q.dim() not in (3, 4):
+        raise _invalid("q must be [batch, q_len, heads, head_dim] or [batch, heads, head_dim]")
+    batch, heads = q.shape[0], q.shape[-2]
+    q_len = q.shape[1] if q.dim() == 4 else 1
+    qp = _takes("q", q, dev, q.dtype, (*q.shape[:-1], d), contiguous=False)
+    qs = _token_rows("q", q, (heads, d))
+    tp = _takes("page_table", page_table, dev, torch.int32, (batch, None))
+    lp = _takes("lengths", lengths, dev, torch.int32, (batch,))
+    max_pages = page_table.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    op = _takes("out", out, dev, q.dtype, q.shape)
+    need = lib.hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
+    if need > 0 and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _on_device("workspace", workspace, dev)
+        _holds("workspace", workspace, max(need, 0))
+    with _on(dev, stream) as s:
+        _check(lib.hadq_kv4_attention(qp, qs, _dtype_code(q.dtype), batch, q_len, heads, kv_heads, d, block, group, *ptrs,
+                                      pages, size, tp, max_pages, lp, d ** -0.5 if scale is None else scale, op,
+                                      None if workspace is None else workspace.data_ptr(),
+                                      0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+    return out

@@ -258,6 +258,126 @@ HADQ_API hadq_status hadq_rotate_quant_codebook(const void* x, hadq_dtype x_dtyp
                                                 const double* thresholds, void* codes, float* norms, void* stream);
 
 /*
+ * The operators on both sides of the int8 codes, and the cache of the rotated
+ * K (R3).  Conventions as above; in these calls every pointer, the scale
+ * vectors, page tables and lengths included, is 16-byte aligned, and sizes
+ * that are not a documented multiple return HADQ_ERR_UNSUPPORTED.
+ */
+
+/*
+ * hadq_rmsnorm_quant: the norm in front of a linear whose input rotation (R1)
+ * is folded into its weights, with the residual's addition and per-token int8
+ * codes ("Rotation Transform", section 1.1: R1 is merged into the weights
+ * around the norm; the codes are HADQ_INT8_SYM's).  For every row
+ *     h = x + residual            (rounded to x_dtype; h = x without residual)
+ *     t = h * weight              (fp32 product)
+ *     q = rne(127 t / max|t|)     in [-127, 127]; all 0 when max|t| = 0
+ *     s = max|t| / (127 sqrt(mean(h^2) + eps))
+ * so that q * s is RMSNorm(h) * weight.  The codes are exact: the norm's
+ * factor cancels in them, and the quotient's rounding is that of the reals.
+ * The sum of squares is held in fp32.
+ *   x, residual   [rows x n] of x_dtype; residual and residual_out are given
+ *                 together or both null
+ *   weight        [n] of x_dtype
+ *   residual_out  [rows x n]: h; may be x or residual itself
+ *   codes         [rows x n] int8;  scales [rows] fp32
+ * n is a multiple of 8, at most 32768.
+ */
+HADQ_API hadq_status hadq_rmsnorm_quant(const void* x, hadq_dtype x_dtype, int64_t rows, int64_t n,
+                                        const void* residual, const void* weight, float eps, void* residual_out,
+                                        int8_t* codes, float* scales, void* stream);
+
+/*
+ * hadq_matmul_int8: the linear that consumes per-token int8 codes (those of
+ * hadq_rmsnorm_quant and of hadq_rotate_quant with HADQ_INT8_SYM):
+ *     out[i][j] = (sum_k a[i][k] w[j][k]) * a_scales[i] * w_scales[j] + bias[j]
+ * The sum is exact (32-bit integers); it is converted to fp32, scaled and
+ * biased in fp32, and rounded once to out_dtype.
+ *   a        [rows x k] int8, a_scales [rows] fp32
+ *   w        [cols x k] int8 (a linear's weight, an output channel per row),
+ *            w_scales [cols] fp32
+ *   bias     [cols] fp32, or null
+ *   out      [rows x cols] of out_dtype
+ * k is a multiple of 16, at most 131056 (the exact 32-bit sums' limit, codes
+ * of -128 included); rows and cols are any.
+ */
+HADQ_API hadq_status hadq_matmul_int8(const int8_t* a, const float* a_scales, int64_t rows, const int8_t* w,
+                                      const float* w_scales, int64_t cols, int64_t k, const float* bias, void* out,
+                                      hadq_dtype out_dtype, void* stream);
+
+/*
+ * The int4 cache of one layer: pages of page_size positions (a multiple of
+ * 16), each of kv_heads heads, for K and for V
+ *   codes  [num_pages][kv_heads][page_size][head_dim / 2]      bytes, nibbles as HADQ_INT4_SYM
+ *   scales [num_pages][kv_heads][page_size][head_dim / group]  fp16
+ * head_dim is 64 or 128, group 32, 64 or 128 and divides it.  Position p of
+ * the cache (a slot) is offset p % page_size of page p / page_size.
+ *
+ * hadq_kv4_append: R3 ("Rotation Transform", section 1.1: K rotated per head
+ * after RoPE, before it enters the cache).  For every token with slots[t] >= 0
+ * each head's K row is rotated (block 0 or head_dim; block 1: not), K and V
+ * are quantized per group and stored at that slot; nothing else in the cache
+ * is written.  Rotation and codes are defined bit for bit: butterfly stages in
+ * ascending order of the index bit in fp32; with M the group's absmax of the
+ * unnormalised sums and c = fp32(1/sqrt(head_dim)) (1 unrotated),
+ *     s = fp16(min(fp32(fp32(M c) / 7), 65504)),  q = clamp(rne(z * fp32(c / s)), -7, 7),
+ * s = 0 giving codes 0: HADQ_INT4_SYM, except that a scale beyond fp16
+ * saturates instead of becoming infinite.
+ *   k, v       row (t, h) at k + t * k_stride + h * head_dim, in elements of
+ *              dtype: slices of a fused projection's output need no copy.
+ *              k_stride, v_stride: at least kv_heads * head_dim, a multiple of
+ *              16 bytes
+ *   slots      [tokens] int64; negative: the token is not stored; at or above
+ *              num_pages * page_size: not stored, and recorded as a fault.
+ *              A slot given twice ends up with either token's rows, or parts
+ *              of both.
+ */
+HADQ_API hadq_status hadq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                     hadq_dtype dtype, int64_t tokens, int64_t kv_heads, int64_t head_dim,
+                                     int64_t block, int64_t group, const int64_t* slots, int64_t num_pages,
+                                     int64_t page_size, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                                     void* stream);
+
+/*
+ * hadq_kv4_attention: attention of each sequence's newest q_len tokens (one,
+ * or a few drafted ones; at most 64) over its cached positions:
+ *     out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q R) . k_j),
+ * R the rotation that K was cached with (block as in hadq_kv4_append: the
+ * query is rotated here), j over the positions the query sees.  Query i of
+ * sequence b is position lengths[b] - q_len + i and sees positions up to its
+ * own; one that sees none (lengths[b] = 0, or a length below q_len) gives 0.
+ *   q          row (b, i, head) at q + (b * q_len + i) * q_stride + head *
+ *              head_dim; HADQ_BF16.  Heads h * heads / kv_heads .. share K/V head h
+ *   page_table [batch][max_pages] int32: pages of a sequence in order; only
+ *              the first ceil(length / page_size) are read.  A page outside
+ *              0 .. num_pages - 1 is recorded as a fault and its positions are
+ *              not attended to
+ *   lengths    [batch] int32: positions, the new ones included (append them
+ *              first); outside 0 .. max_pages * page_size: clamped, and
+ *              recorded as a fault
+ *   out        [batch][q_len][heads][head_dim] bf16
+ *   workspace  hadq_kv4_attention_workspace(..., max_pages * page_size) bytes
+ *              of device memory (null when that is 0), written and read by
+ *              this call: calls that may run at the same time need one each
+ * Positions beyond a length are never read as numbers: any bits may lie there.
+ * Scores, sums and the output accumulate in fp32; q (scaled by a power of 2)
+ * and the probabilities are rounded to fp16 for the products, whose other side,
+ * the codes, is exact.  Results do not depend on the order of execution.
+ */
+HADQ_API hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype, int64_t batch,
+                                        int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                        int64_t block, int64_t group, const void* k_codes, const void* k_scales,
+                                        const void* v_codes, const void* v_scales, int64_t num_pages,
+                                        int64_t page_size, const int32_t* page_table, int64_t max_pages,
+                                        const int32_t* lengths, float scale, void* out, void* workspace,
+                                        int64_t workspace_bytes, void* stream);
+
+/* Bytes of hadq_kv4_attention's workspace for sequences of up to max_positions
+ * positions (max_pages * page_size); -1 for sizes the call does not take. */
+HADQ_API int64_t hadq_kv4_attention_workspace(int64_t batch, int64_t q_len, int64_t heads, int64_t kv_heads,
+                                              int64_t head_dim, int64_t max_positions);
+
+/*
  * hadq_rotate_quant_host: the same operation on HOST buffers.  Enqueues on
  * `stream`: copy x_host -> x_dev, hadq_rotate_quant on the device buffers,
  * copy codes_dev -> codes_host and scales_dev -> scales_host.  The caller
@@ -331,8 +451,9 @@ HADQ_API const char* hadq_status_string(hadq_status status);
 /* One-line reason for the calling thread's most recent failed call ("" if none). */
 HADQ_API const char* hadq_last_error(void);
 
-/* Fault bits recorded by kernels whose bounded internal waits ran out (0 when
- * every wait completed; -1 if the flag could not be read).  Synchronous:
+/* Fault bits recorded by kernels whose bounded internal waits ran out, or that
+ * met a page (16), a length (32) or a slot (64) outside the cache (0 when
+ * nothing did; -1 if the flag could not be read).  Synchronous:
  * call after the work of interest has completed.  `clear` != 0 resets the
  * flags.  No paper counterpart: a diagnostic of this implementation. */
 HADQ_API int hadq_device_faults(int clear);
