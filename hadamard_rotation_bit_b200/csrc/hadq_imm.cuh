@@ -1,12 +1,39 @@
 // Matrix product of int8 codes with a scale per token and per output channel:
-//   y[i][j] = (sum_k a[i][k] w[j][k]) * sa[i] * sw[j] + bias[j].
-// The sum is exact in 32-bit integers (k < 131072), so its order is free.
+//
+//   y[i][j] = (sum_k a[i][k] w[j][k]) * sa[i] * sw[j] + bias[j],
+//
+// on the tensor cores (tcgen05.mma kind::i8, 32-bit integer sums in tensor
+// memory).  The sums are exact for k < 131072, so their order is free: a split
+// of k adds up to the same bits, and every kernel here gives the same result.
+//
+// Two kernels.  Both stage 128-byte slices of k by TMA (128-byte swizzle; the
+// tail of k and rows beyond a matrix are filled with zeros) into a ring that
+// one thread feeds and one thread consumes.
+//
+//   imm_split_kernel  few tokens: bound by reading w.  Output channels are the
+//       MMA's 128 rows and TN tokens its columns, so one token costs no more
+//       traffic than it has, and the CTAs of a cluster share the k of a tile,
+//       adding their sums through distributed shared memory.
+//   imm_pair_kernel   many tokens: bound by the tensor cores.  CTA pairs
+//       compute 256 x 256 tiles (cta_group::2), which halves the shared-memory
+//       and L2 reads per product of a single CTA's tile; persistent, two
+//       accumulators, so that the epilogue of a tile runs under the products
+//       of the next.
 #pragma once
 
-#include "hadq_device.cuh"
+#include "hadq_tc.cuh"
 
 namespace hadq {
 namespace imm {
+
+using tc::mbar_arrive_expect_tx;
+using tc::mbar_init;
+using tc::mbar_wait;
+using tc::smem_desc;
+using tc::smem_u32;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::tmem_wait_ld;
 
 struct Args {
   const int8_t* a;
@@ -15,45 +42,439 @@ struct Args {
   const float* sw;
   const float* bias;   // nullptr: none
   void* out;
-  int m, n, k;
+  int m, n, k;         // tokens, channels
 };
 
-// 64 x 64 outputs per CTA, four-way byte products.
+constexpr int kSlice = 128;   // bytes of k per stage
+
+// Instruction descriptor of kind::i8: signed A and B, 32-bit integer D, both
+// operands K-major.
+__host__ __device__ constexpr uint32_t idesc_i8(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc),
+        "r"(accumulate));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc),
+        "r"(accumulate));
+}
+
+// 32 consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld32i(uint32_t taddr, int (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// Address in the cluster's shared memory of `addr` (this CTA's) in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// (sum * sa) * sw + bias, rounded step by step, so that every kernel's result
+// is the same.
+__device__ __forceinline__ float scaled(int acc, float sa) { return __fmul_rn(__int2float_rn(acc), sa); }
+__device__ __forceinline__ float finish(float t, float sw, bool biased, float bias) {
+  const float y = __fmul_rn(t, sw);
+  return biased ? __fadd_rn(y, bias) : y;
+}
+
 template <bool OUT_BF16>
-__global__ void __launch_bounds__(256) imm_plain_kernel(const __grid_constant__ Args p) {
-  __shared__ int as[64][17], ws[64][17];
-  grid_dependency_sync();
-  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < p.k; k0 += 64) {
-    const int rr = threadIdx.x >> 2, cc = threadIdx.x & 3;
-    int4 va = make_int4(0, 0, 0, 0), vw = va;
-    if (k0 + cc * 16 < p.k) {
-      if (i0 + rr < p.m) va = *reinterpret_cast<const int4*>(p.a + static_cast<int64_t>(i0 + rr) * p.k + k0 + cc * 16);
-      if (j0 + rr < p.n) vw = *reinterpret_cast<const int4*>(p.w + static_cast<int64_t>(j0 + rr) * p.k + k0 + cc * 16);
+__device__ __forceinline__ void store_one(void* out, int64_t e, float y) {
+  if constexpr (OUT_BF16) static_cast<__nv_bfloat16*>(out)[e] = __float2bfloat16_rn(y);
+  else static_cast<float*>(out)[e] = y;
+}
+
+// ------------------------------------------------------------- few tokens
+
+template <int TN_, int STAGES_>
+struct SplitCfg {
+  static constexpr int TN = TN_, STAGES = STAGES_;
+  static constexpr int W_BYTES = 128 * kSlice, A_BYTES = TN * kSlice;
+  static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;
+  static constexpr int TMEM_COLS = TN < 32 ? 32 : TN;
+  static constexpr int THREADS = 128;
+  static constexpr int SM_RING = 0;
+  static constexpr int SM_JOIN = STAGES * STAGE_BYTES;                // [source rank][column / 4 of mine][channel][4]
+  static constexpr int SM_BARS = SM_JOIN + TN * 128 * 4;
+  static constexpr int SM_SLOT = SM_BARS + 8 * (2 * STAGES + 1);
+  static constexpr int SMEM_BYTES = SM_SLOT + 16 + 1024;
+};
+
+// CTA (tile, rank): channels ch0 .. ch0 + 127, tokens t0 .. t0 + TN - 1, the
+// rank's share of k.  Every rank then finishes TN / splits of the tokens.
+template <class C, bool OUT_BF16>
+__global__ void __launch_bounds__(C::THREADS)
+imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                 const __grid_constant__ Args p, int splits, int token_tiles) {
+  constexpr int TN = C::TN, STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = tc::smem_align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::SM_BARS);
+  uint64_t* empty = full + STAGES;
+  uint64_t* done = empty + STAGES;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::SM_SLOT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int rank = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = blockIdx.x / splits;
+  const int ch0 = (tile / token_tiles) * 128, t0 = (tile % token_tiles) * TN;
+  const int slices = (p.k + kSlice - 1) / kSlice;
+  const int s0 = static_cast<int>(static_cast<int64_t>(slices) * rank / splits);
+  const int iters = static_cast<int>(static_cast<int64_t>(slices) * (rank + 1) / splits) - s0;   // >= 1
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    as[rr][cc * 4] = va.x, as[rr][cc * 4 + 1] = va.y, as[rr][cc * 4 + 2] = va.z, as[rr][cc * 4 + 3] = va.w;
-    ws[rr][cc * 4] = vw.x, ws[rr][cc * 4 + 1] = vw.y, ws[rr][cc * 4 + 2] = vw.z, ws[rr][cc * 4 + 3] = vw.w;
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[u][v] = __dp4a(as[ty + 16 * u][kk], ws[tx + 16 * v][kk], acc[u][v]);
-    __syncthreads();
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const int i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-      if (i >= p.m || j >= p.n) continue;
-      float y = __int2float_rn(acc[u][v]) * p.sa[i] * p.sw[j];
-      if (p.bias) y += p.bias[j];
-      const int64_t e = static_cast<int64_t>(i) * p.n + j;
-      if constexpr (OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(y);
-      else static_cast<float*>(p.out)[e] = y;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(C::TMEM_COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  if (splits > 1) cluster_arrive();           // matched before the first access to another CTA's memory
+  grid_dependency_sync();
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------- producer
+    for (int i = 0; i < iters; ++i) {
+      const int s = i % STAGES;
+      if (i >= STAGES && !mbar_wait(&empty[s], ((i / STAGES) & 1) ^ 1)) {
+        atomicOr(&tc::hadq_tc_fault, tc::kFaultProducer);
+        tc::drain_loads(full, STAGES, i);
+        break;
+      }
+      mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+      uint8_t* dst = smem + C::SM_RING + s * C::STAGE_BYTES;
+      tc::tma_load_2d(dst, &map_w, (s0 + i) * kSlice, ch0, &full[s]);
+      tc::tma_load_2d(dst + C::W_BYTES, &map_a, (s0 + i) * kSlice, t0, &full[s]);
     }
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------------------ MMA
+    int i = 0;
+    for (; i < iters; ++i) {
+      const int s = i % STAGES;
+      if (!mbar_wait(&full[s], (i / STAGES) & 1)) {
+        atomicOr(&tc::hadq_tc_fault, tc::kFaultMma);
+        tc::drain_mmas(empty, STAGES, i);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t wb = smem_u32(smem + C::SM_RING + s * C::STAGE_BYTES), ab = wb + C::W_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < kSlice / 32; ++kk)
+        mma_i8<1>(tmem, smem_desc(wb + 32 * kk, 16, 1024, tc::kSwizzle128), smem_desc(ab + 32 * kk, 16, 1024, tc::kSwizzle128),
+                  idesc_i8(128, TN), (i | kk) != 0 ? 1u : 0u);
+      tc::mma_commit(&empty[s]);
+    }
+    if (i == iters) tc::mma_commit(done);
+  }
+  __syncwarp();
+
+  // --------------------------------------------------------------- epilogue
+  bool ok = mbar_wait(done, 0);
+  if (!ok && lane == 0) atomicOr(&tc::hadq_tc_fault, tc::kFaultEpilogue);
+  ok = __all_sync(0xffffffffu, ok);
+  tc_fence_after();
+  const int ch = ch0 + threadIdx.x;           // TMEM lane = thread
+  const bool live = ch < p.n;
+  const float sw = live ? p.sw[ch] : 0.f;
+  const float bias = live && p.bias != nullptr ? p.bias[ch] : 0.f;
+  auto put = [&](int token, int acc) {
+    if (!live || token >= p.m) return;
+    store_one<OUT_BF16>(p.out, static_cast<int64_t>(token) * p.n + ch,
+                        finish(scaled(acc, p.sa[token]), sw, p.bias != nullptr, bias));
+  };
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  if (splits == 1) {
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < TN; c += 16) {
+        int v[16];
+        tmem_ld16i(taddr + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) put(t0 + c + j, v[j]);
+      }
+    }
+  } else {
+    // Token column c goes to rank c / mine; there, the sources' sums are added
+    // (integers: in any order the same).
+    const int mine = TN / splits;             // 2 or more, a power of 2
+    cluster_wait();
+    const uint32_t join = smem_u32(smem + C::SM_JOIN) + (rank * mine * 128 + threadIdx.x) * 4;
+#pragma unroll 1
+    for (int c = 0; c < TN; c += 16) {
+      int v[16];
+      if (ok) {
+        tmem_ld16i(taddr + c, v);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int to = (c + j) / mine, col = (c + j) % mine;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(join + col * 512, to)), "r"(ok ? v[j] : 0) : "memory");
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    const int* got = reinterpret_cast<const int*>(smem + C::SM_JOIN) + threadIdx.x;
+    for (int col = 0; col < mine; ++col) {
+      int sum = 0;
+      for (int r = 0; r < splits; ++r) sum += got[(r * mine + col) * 128];
+      put(t0 + rank * mine + col, sum);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+  }
+}
+
+// ------------------------------------------------------------ many tokens
+
+struct PairCfg {
+  static constexpr int STAGES = 6;
+  static constexpr int TILE = 256;                                    // tokens and channels of a pair's tile
+  static constexpr int OP_BYTES = 128 * kSlice;                       // one CTA's half of an operand
+  static constexpr int STAGE_BYTES = 2 * OP_BYTES;
+  static constexpr int THREADS = 32 * 6;                              // producer, MMA, four epilogue warps
+  static constexpr int SM_RING = 0;
+  static constexpr int SM_BARS = STAGES * STAGE_BYTES;
+  static constexpr int SM_SLOT = SM_BARS + 8 * (2 * STAGES + 4);
+  static constexpr int SM_TURN = SM_SLOT + 16;                        // per epilogue warp: 32 rows x 33 words
+  static constexpr int SMEM_BYTES = SM_TURN + 4 * 32 * 33 * 4 + 1024;
+};
+
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs of the pair once the
+// MMAs issued so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Tile t of the grid: bands of 8 token tiles, channels outer, so that the
+// tiles in flight share their operands in L2.
+__device__ __forceinline__ void tile_at(int t, int mt, int nt, int* im, int* in) {
+  const int band = 8 * nt, b = t / band, rest = t - b * band;
+  const int h = min(8, mt - 8 * b);
+  *in = rest / h;
+  *im = 8 * b + rest - *in * h;
+}
+
+template <bool OUT_BF16>
+__global__ void __launch_bounds__(PairCfg::THREADS, 1)
+imm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ Args p) {
+  using C = PairCfg;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = tc::smem_align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::SM_BARS);    // used in the first CTA of the pair
+  uint64_t* empty = full + STAGES;                                    // in both
+  uint64_t* acc_full = empty + STAGES;                                // in both
+  uint64_t* acc_empty = acc_full + 2;                                 // in the first
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::SM_SLOT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);                                    // four epilogue warps of each CTA
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::);
+  }
+  tc_fence_before();
+  cluster_arrive();                                                   // barriers and tensor memory of both are ready
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  grid_dependency_sync();
+
+  const int mt = (p.m + C::TILE - 1) / C::TILE, nt = (p.n + C::TILE - 1) / C::TILE;
+  const int tiles = mt * nt, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int slices = (p.k + kSlice - 1) / kSlice;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ----------------------------------------------- producer, both CTAs
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        int im, in;
+        tile_at(t, mt, nt, &im, &in);
+        const int row_a = im * C::TILE + rank * 128, row_w = in * C::TILE + rank * 128;
+        for (int i = 0; i < slices; ++i, ++it) {
+          const int s = it % STAGES;
+          if (it >= STAGES && !mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1)) {
+            atomicOr(&tc::hadq_tc_fault, tc::kFaultProducer);
+            if (rank == 0) tc::drain_loads(full, STAGES, it);
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);   // the loads of both CTAs
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+          uint8_t* dst = smem + C::SM_RING + s * C::STAGE_BYTES;
+          tma_load_pair(dst, &map_a, i * kSlice, row_a, bar);
+          tma_load_pair(dst + C::OP_BYTES, &map_w, i * kSlice, row_w, bar);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // --------------------------------------------------- MMA, first CTA
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs, ++n) {
+        const uint32_t b = n & 1;
+        if (n >= 2 && !mbar_wait(&acc_empty[b], ((n >> 1) & 1) ^ 1)) ok = false;
+        tc_fence_after();
+        for (int i = 0; ok && i < slices; ++i, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(&full[s], (it / STAGES) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ab = smem_u32(smem + C::SM_RING + s * C::STAGE_BYTES), wb = ab + C::OP_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < kSlice / 32; ++kk)
+            mma_i8<2>(tmem + b * 256, smem_desc(ab + 32 * kk, 16, 1024, tc::kSwizzle128),
+                      smem_desc(wb + 32 * kk, 16, 1024, tc::kSwizzle128), idesc_i8(256, 256), (i | kk) != 0 ? 1u : 0u);
+          commit_pair(&empty[s]);
+        }
+        if (ok) {
+          commit_pair(&acc_full[b]);
+        } else {
+          atomicOr(&tc::hadq_tc_fault, tc::kFaultMma);
+          tc::drain_mmas(empty, STAGES, it);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------- epilogue, both CTAs
+    const int quarter = warp & 3;
+    uint32_t n = 0;
+    float* turn = reinterpret_cast<float*>(smem + C::SM_TURN) + (warp - 2) * 32 * 33;
+    const uint32_t release = map_rank(smem_u32(acc_empty), 0);
+    for (int t = pair; t < tiles; t += pairs, ++n) {
+      int im, in;
+      tile_at(t, mt, nt, &im, &in);
+      const uint32_t b = n & 1;
+      const bool ok = mbar_wait(&acc_full[b], (n >> 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) atomicOr(&tc::hadq_tc_fault, tc::kFaultEpilogue);
+        break;
+      }
+      tc_fence_after();
+      const int row0 = im * C::TILE + rank * 128 + quarter * 32, col0 = in * C::TILE;
+      const int row = row0 + lane;
+      const float sa = row < p.m ? p.sa[row] : 0.f;
+      const uint32_t taddr = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < C::TILE; c += 32) {
+        int v[32];
+        tmem_ld32i(taddr + c, v);
+        tmem_wait_ld();
+        if (c + 32 == C::TILE) {                                      // the last read: the MMAs may overwrite
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(release + 8 * b) : "memory");
+        }
+        const int col = col0 + c;
+        if (col >= p.n) continue;
+        // Scales of the 32 columns: lane c's, passed around; rows turned so
+        // that a warp stores runs of columns (any n, any alignment).
+        const bool in_n = col + lane < p.n;
+        const float sw = in_n ? p.sw[col + lane] : 0.f;
+        const float bias = in_n && p.bias != nullptr ? p.bias[col + lane] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = scaled(v[j], sa);
+        __syncwarp();
+        const int rows = min(32, p.m - row0);
+        for (int r = 0; r < rows; ++r) {
+          if (in_n)
+            store_one<OUT_BF16>(p.out, static_cast<int64_t>(row0 + r) * p.n + col + lane,
+                                finish(turn[r * 33 + lane], sw, p.bias != nullptr, bias));
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // Neither CTA leaves while the other may reach its barriers or operands.
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
 }
 
 }  // namespace imm

@@ -103,9 +103,21 @@ struct NormVariant {
 };
 NormVariant norm_kernel_for(bool bf16, bool residual, int64_t rows, int64_t n);
 
-// int8 matrix product.
-using ImmFn = void (*)(const imm::Args);
-ImmFn imm_plain_for(bool out_bf16);
+// int8 matrix product: the kernel for few tokens (up to `tokens` per CTA) and
+// the one for many.
+using ImmSplitFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args, int, int);
+using ImmPairFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args);
+struct ImmSplitVariant {
+  ImmSplitFn fn;
+  int threads, smem, tokens;
+};
+struct ImmPairVariant {
+  ImmPairFn fn;
+  int threads, smem;
+};
+ImmSplitVariant imm_split_for(int64_t m, bool out_bf16);
+ImmPairVariant imm_pair_for(bool out_bf16);
+int imm_fault_bits(int clear);
 
 // int4 cache: append, attention (rows = query rows per K/V head; the variant
 // takes `rows` of them per CTA) and the join of its splits.

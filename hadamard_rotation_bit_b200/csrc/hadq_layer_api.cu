@@ -47,7 +47,53 @@ hadq_status disjoint(const Span* outs, int nouts, const Span* ins, int nins, con
 constexpr int64_t kMaxNormN = 32768;
 constexpr int64_t kMaxK = 131071;        // 128 * 128 * k < 2^31
 constexpr int64_t kMaxDim = int64_t(1) << 30;
-constexpr int64_t kMaxGridY = 65535;
+
+// A tensor map over a row-major int8 matrix: boxes of 128 bytes of k times
+// `box_rows` rows, 128-byte swizzle, zeros outside.
+hadq_status int8_map(const int8_t* p, int64_t rows, int64_t k, int box_rows, CUtensorMap* map) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (encode == nullptr) return fail(HADQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(hadq::imm::kSlice), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HADQ_OK : fail(HADQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
+hadq_status launch_imm(const hadq::imm::Args& p, bool out_bf16, cudaStream_t stream) {
+  int sms = 0, dev = 0, occ = 0;
+  hadq_status st = device_sms(&sms, &dev);
+  if (st != HADQ_OK) return st;
+  CUtensorMap map_a, map_w;
+  const int64_t pair_tiles = ceil_div(p.m, 256) * ceil_div(p.n, 256);
+  if (p.m > 128 && pair_tiles >= 40) {
+    const hl::ImmPairVariant v = hl::imm_pair_for(out_bf16);
+    st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
+    if (st == HADQ_OK) st = int8_map(p.a, p.m, p.k, 128, &map_a);
+    if (st == HADQ_OK) st = int8_map(p.w, p.n, p.k, 128, &map_w);
+    if (st != HADQ_OK) return st;
+    if (pair_tiles > INT32_MAX) return unsupported("too many output tiles");
+    const int64_t grid = 2 * std::min<int64_t>(pair_tiles, sms / 2);
+    return launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(grid)), 2, v.threads, v.smem, stream, map_a, map_w, p),
+                         "int8 matrix product launch");
+  }
+  const hl::ImmSplitVariant v = hl::imm_split_for(p.m, out_bf16);
+  st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
+  if (st == HADQ_OK) st = int8_map(p.a, p.m, p.k, v.tokens, &map_a);
+  if (st == HADQ_OK) st = int8_map(p.w, p.n, p.k, 128, &map_w);
+  if (st != HADQ_OK) return st;
+  const int64_t token_tiles = ceil_div(p.m, v.tokens), tiles = ceil_div(p.n, 128) * token_tiles;
+  const int64_t slices = ceil_div(p.k, hadq::imm::kSlice);
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= int64_t(sms) * occ && slices >= 8 * splits) splits *= 2;
+  if (tiles * splits > INT32_MAX) return unsupported("too many output tiles");
+  return launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(tiles * splits)), splits, v.threads, v.smem, stream, map_w,
+                                   map_a, p, splits, static_cast<int>(token_tiles)),
+                       "int8 matrix product launch");
+}
 
 // What the two cache entry points share.
 struct Cache {
@@ -183,10 +229,7 @@ hadq_status hadq_matmul_int8(const int8_t* a, const float* a_scales, int64_t row
     if (st != HADQ_OK) return st;
     const hadq::imm::Args p{a, w, a_scales, w_scales, bias, out, static_cast<int>(rows), static_cast<int>(cols),
                             static_cast<int>(k)};
-    const dim3 grid(static_cast<unsigned>(ceil_div(cols, 64)), static_cast<unsigned>(ceil_div(rows, 64)));
-    return launch_result(launch_pdl3(hl::imm_plain_for(out_dtype == HADQ_BF16), grid, 1, 256, 0,
-                                     static_cast<cudaStream_t>(stream), p),
-                         "int8 matrix product launch");
+    return launch_imm(p, out_dtype == HADQ_BF16, static_cast<cudaStream_t>(stream));
   });
 }
 

@@ -461,8 +461,10 @@ def _invalid(message: str) -> HadqError:
 
 def _takes(name: str, t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape, contiguous: bool = True) -> int:
     """Address of a tensor that must have this device, dtype and shape (None: any extent)."""
-    if not t.is_cuda or t.device != dev:
-        _on_device(name, t, dev)
+    if t.dtype is dtype and t.shape == shape and t.device == dev and dev.type == "cuda":
+        if not contiguous or t.is_contiguous():
+            return t.data_ptr()
+    _on_device(name, t, dev)
     if t.dtype != dtype:
         raise _invalid(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != len(shape) or any(s is not None and s != g for s, g in zip(shape, t.shape)):
@@ -472,25 +474,20 @@ def _takes(name: str, t: torch.Tensor, dev: torch.device, dtype: torch.dtype, sh
     return t.data_ptr()
 
 
-class _on:
-    """Device of a call made current for it, and its stream: the one given, or
-    that device's current stream.  Outputs are allocated under it, so a stream
-    given explicitly is the caller's to order with their use, as elsewhere."""
-
-    __slots__ = ("guard", "handle")
-
-    def __init__(self, dev: torch.device, stream):
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self.handle = _stream_handle(torch.cuda.current_stream(dev) if stream is None else stream)
-
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, dev: torch.device, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current: on the stream given,
+    or on that device's current stream.  Outputs come from that device's
+    allocator, so a stream given explicitly is the caller's to order with their
+    use, as elsewhere."""
+    index = dev.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != HADQ_OK:
+        _check(status)
 
 
 def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -499,29 +496,26 @@ def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     """RMSNorm(x + residual) * weight as int8 codes with a scale per token (see
     include/hadq.h).  Returns (codes, scales, residual_out); the last is
     x + residual, or None without a residual.  residual_out may be x or residual."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, n = _rows_n(x)
-    dev = x.device
-    _on_device("x", x, dev)
-    w = _takes("weight", weight, dev, x.dtype, (n,))
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    xp = _takes("x", x, dev, dtype, shape)
+    wp = _takes("weight", weight, dev, dtype, (n,))
+    rp = op = None
     if residual is not None:
-        _takes("residual", residual, dev, x.dtype, x.shape)
+        rp = _takes("residual", residual, dev, dtype, shape)
         if residual_out is None:
             residual_out = torch.empty_like(x)
-        _takes("residual_out", residual_out, dev, x.dtype, x.shape)
+        op = _takes("residual_out", residual_out, dev, dtype, shape)
     elif residual_out is not None:
         raise _invalid("residual_out needs a residual")
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
-    _takes("codes", codes, dev, torch.int8, x.shape)
+        codes = torch.empty_like(x, dtype=torch.int8)
     if scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    _takes("scales", scales, dev, torch.float32, x.shape[:-1])
-    with _on(dev, stream) as s:
-        _check(lib.hadq_rmsnorm_quant(x.data_ptr(), _dtype_code(x.dtype), rows, n,
-                                      None if residual is None else residual.data_ptr(), w, eps,
-                                      None if residual is None else residual_out.data_ptr(), codes.data_ptr(),
-                                      scales.data_ptr(), s))
+        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    cp = _takes("codes", codes, dev, torch.int8, shape)
+    sp = _takes("scales", scales, dev, torch.float32, shape[:-1])
+    _call(lib.hadq_rmsnorm_quant, dev, stream, xp, _dtype_code(dtype), rows, n, rp, wp, eps, op, cp, sp)
     return codes, scales, residual_out
 
 
@@ -530,21 +524,19 @@ def hadq_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """(a . w^T) * a_scales[:, None] * w_scales + bias of int8 codes a [..., k]
     and weights w [cols, k] (see include/hadq.h)."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, k = _rows_n(a)
-    dev = a.device
-    _on_device("a", a, dev)
+    dev, lead = a.device, a.shape[:-1]
     ap = _takes("a", a, dev, torch.int8, a.shape)
-    asp = _takes("a_scales", a_scales, dev, torch.float32, a.shape[:-1])
-    wp = _takes("w", w, dev, torch.int8, (None, k))
-    cols = w.shape[0]
+    asp = _takes("a_scales", a_scales, dev, torch.float32, lead)
+    cols = w.shape[0] if w.dim() else 0
+    wp = _takes("w", w, dev, torch.int8, (cols, k))
     wsp = _takes("w_scales", w_scales, dev, torch.float32, (cols,))
     bp = None if bias is None else _takes("bias", bias, dev, torch.float32, (cols,))
     if out is None:
-        out = torch.empty((*a.shape[:-1], cols), dtype=out_dtype, device=dev)
-    op = _takes("out", out, dev, out.dtype, (*a.shape[:-1], cols))
-    with _on(dev, stream) as s:
-        _check(lib.hadq_matmul_int8(ap, asp, rows, wp, wsp, cols, k, bp, op, _dtype_code(out.dtype), s))
+        out = torch.empty((*lead, cols), dtype=out_dtype, device=dev)
+    op = _takes("out", out, dev, out.dtype, (*lead, cols))
+    _call(lib.hadq_matmul_int8, dev, stream, ap, asp, rows, wp, wsp, cols, k, bp, op, _dtype_code(out.dtype))
     return out
 
 
@@ -556,28 +548,31 @@ def _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales):
     groups = k_scales.shape[3]
     if groups == 0 or (2 * half) % groups:
         raise _invalid(f"{groups} scales for {2 * half} elements")
-    ptrs = [_takes(name, t, dev, dtype, (pages, heads, size, last))
-            for name, t, dtype, last in (("k_codes", k_codes, torch.uint8, half), ("k_scales", k_scales, torch.float16, groups),
-                                         ("v_codes", v_codes, torch.uint8, half), ("v_scales", v_scales, torch.float16, groups))]
+    cs, ss = k_codes.shape, (pages, heads, size, groups)
+    ptrs = (_takes("k_codes", k_codes, dev, torch.uint8, cs), _takes("k_scales", k_scales, dev, torch.float16, ss),
+            _takes("v_codes", v_codes, dev, torch.uint8, cs), _takes("v_scales", v_scales, dev, torch.float16, ss))
     return ptrs, pages, heads, size, 2 * half, 2 * half // groups
 
 
 def _token_rows(name: str, x: torch.Tensor, tail) -> int:
     """Elements between the tokens of x [..., heads, head_dim]: heads and their
     elements dense, tokens (all leading dimensions) evenly spaced."""
-    width = tail[0] * tail[1]
-    if x.stride(-1) != 1 or x.stride(-2) != tail[1]:
+    width, stride = tail[0] * tail[1], x.stride()
+    if stride[-1] != 1 or stride[-2] != tail[1]:
         raise _invalid(f"{name}: the last two dimensions must be dense")
-    stride, step = None, 1
-    for d in range(x.dim() - 3, -1, -1):
-        if x.shape[d] > 1:
-            if stride is None:
-                stride = x.stride(d)
-            elif x.stride(d) != stride * step:
+    shape = x.shape
+    if len(shape) == 3:
+        return stride[0] if shape[0] > 1 else width
+    spacing, step = None, 1
+    for d in range(len(shape) - 3, -1, -1):
+        if shape[d] > 1:
+            if spacing is None:
+                spacing = stride[d]
+            elif stride[d] != spacing * step:
                 raise _invalid(f"{name}: tokens must be evenly spaced")
-        if stride is not None:
-            step *= x.shape[d]
-    return width if stride is None else stride
+        if spacing is not None:
+            step *= shape[d]
+    return width if spacing is None else spacing
 
 
 def hadq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
@@ -587,17 +582,16 @@ def hadq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cod
     and store both at ``slots`` of the paged int4 cache (see include/hadq.h).
     k, v: [tokens, kv_heads, head_dim], tokens at any even spacing; slots: int64,
     negative for tokens that are not stored."""
-    lib = load_library()
-    dev = k.device
+    lib = _lib or load_library()
+    dev, dtype = k.device, k.dtype
     ptrs, pages, heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
-    kp = _takes("k", k, dev, k.dtype, (None, heads, d), contiguous=False)
-    tokens = k.shape[0]
-    vp = _takes("v", v, dev, k.dtype, (tokens, heads, d), contiguous=False)
+    tokens = k.shape[0] if k.dim() else 0
+    kp = _takes("k", k, dev, dtype, (tokens, heads, d), contiguous=False)
+    vp = _takes("v", v, dev, dtype, (tokens, heads, d), contiguous=False)
     ks, vs = _token_rows("k", k, (heads, d)), _token_rows("v", v, (heads, d))
     sp = _takes("slots", slots, dev, torch.int64, (tokens,))
-    with _on(dev, stream) as s:
-        _check(lib.hadq_kv4_append(kp, ks, vp, vs, _dtype_code(k.dtype), tokens, heads, d, block, group, sp, pages, size,
-                                   *ptrs, s))
+    _call(lib.hadq_kv4_append, dev, stream, kp, ks, vp, vs, _dtype_code(dtype), tokens, heads, d, block, group, sp, pages,
+          size, *ptrs)
 
 
 def hadq_kv4_attention_workspace(batch: int, q_len: int, heads: int, kv_heads: int, head_dim: int,
@@ -616,30 +610,30 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
     """Attention of each sequence's newest tokens q [batch, q_len, heads, head_dim]
     (or [batch, heads, head_dim]) over the paged int4 cache (see include/hadq.h).
     scale: 1 / sqrt(head_dim) when None.  Without ``workspace`` one is allocated."""
-    lib = load_library()
-    dev = q.device
+    lib = _lib or load_library()
+    dev, dtype, shape = q.device, q.dtype, q.shape
     ptrs, pages, kv_heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
-    if q.dim() not in (3, 4):
+    if len(shape) not in (3, 4):
         raise _invalid("q must be [batch, q_len, heads, head_dim] or [batch, heads, head_dim]")
-    batch, heads = q.shape[0], q.shape[-2]
-    q_len = q.shape[1] if q.dim() == 4 else 1
-    qp = _takes("q", q, dev, q.dtype, (*q.shape[:-1], d), contiguous=False)
+    batch, heads = shape[0], shape[-2]
+    q_len = shape[1] if len(shape) == 4 else 1
+    qp = _takes("q", q, dev, dtype, (*shape[:-1], d), contiguous=False)
     qs = _token_rows("q", q, (heads, d))
-    tp = _takes("page_table", page_table, dev, torch.int32, (batch, None))
+    max_pages = page_table.shape[1] if page_table.dim() == 2 else 0
+    tp = _takes("page_table", page_table, dev, torch.int32, (batch, max_pages))
     lp = _takes("lengths", lengths, dev, torch.int32, (batch,))
-    max_pages = page_table.shape[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    op = _takes("out", out, dev, q.dtype, q.shape)
-    need = lib.hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
-    if need > 0 and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    op = _takes("out", out, dev, dtype, shape)
+    nbytes, ws = 0, None
+    if workspace is None:
+        need = lib.hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         _on_device("workspace", workspace, dev)
-        _holds("workspace", workspace, max(need, 0))
-    with _on(dev, stream) as s:
-        _check(lib.hadq_kv4_attention(qp, qs, _dtype_code(q.dtype), batch, q_len, heads, kv_heads, d, block, group, *ptrs,
-                                      pages, size, tp, max_pages, lp, d ** -0.5 if scale is None else scale, op,
-                                      None if workspace is None else workspace.data_ptr(),
-                                      0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+        _holds("workspace", workspace, 0)
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(lib.hadq_kv4_attention, dev, stream, qp, qs, _dtype_code(dtype), batch, q_len, heads, kv_heads, d, block, group,
+          *ptrs, pages, size, tp, max_pages, lp, d ** -0.5 if scale is None else scale, op, ws, nbytes)
     return out

@@ -147,7 +147,8 @@ def check_matmul(out, a, sa, w, sw, bias):
                                    (33, 130, 96), (48, 1433, 4096), (64, 384, 1040), (65, 96, 208), (127, 255, 256),
                                    (128, 256, 64), (129, 257, 80), (200, 1024, 4096), (256, 128, 2048), (257, 511, 640),
                                    (333, 1001, 4112), (512, 4096, 1024), (1025, 520, 384), (2000, 24, 256),
-                                   (40, 20000, 64), (300, 8, 16)])
+                                   (40, 20000, 64), (300, 8, 16), (1300, 2100, 208), (300, 5201, 4112), (200, 10250, 64),
+                                   (10300, 40, 96), (2048, 2048, 1024), (2817, 1032, 272)])
 def test_matmul(m, n, k, out):
     g = gen(m + n + k)
     a = torch.randint(-127, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
