@@ -43,7 +43,8 @@ struct AppendArgs {
 };
 
 // Eight codes of v * f, clamped to +-7: each exact product rounded once onto
-// the integer grid.
+// the integer grid.  For scales that were rounded far (subnormal or saturated);
+// the others cannot reach 7.5 and take pack_int4x8.
 __device__ __forceinline__ uint32_t int4_codes8(const float* v, float f) {
   uint32_t w = 0;
 #pragma unroll
@@ -85,11 +86,11 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
     fwht_bits<32, 0, 5>(v);
 #pragma unroll
     for (int b = 1; b < LPR; b <<= 1) {
-      const bool upper = part & b;
+      const float sgn = (part & b) ? -1.f : 1.f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float o = __shfl_xor_sync(0xffffffffu, v[i], b);
-        v[i] = upper ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
+        v[i] = fmaf(v[i], sgn, o);              // v + o or o - v: one rounding either way
       }
     }
   }
@@ -104,10 +105,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
   const uint32_t off = static_cast<uint32_t>(slot) - page * a.page_size;
   const int64_t cell = (static_cast<int64_t>(page) * a.kv_heads + head) * a.page_size + off;
   uint4 w;
-  w.x = int4_codes8(v, f);
-  w.y = int4_codes8(v + 8, f);
-  w.z = int4_codes8(v + 16, f);
-  w.w = int4_codes8(v + 24, f);
+  if (m * f < 7.25f)
+    w = make_uint4(pack_int4x8<false>(v, 0, f), pack_int4x8<false>(v, 8, f), pack_int4x8<false>(v, 16, f), pack_int4x8<false>(v, 24, f));
+  else
+    w = make_uint4(int4_codes8(v, f), int4_codes8(v + 8, f), int4_codes8(v + 16, f), int4_codes8(v + 24, f));
   *reinterpret_cast<uint4*>(a.codes[which] + cell * (D / 2) + part * 16) = w;
   const int lanes = a.group / 32;                           // lanes per group
   if (part % lanes == 0) a.scales[which][cell * (D / a.group) + part / lanes] = s16;

@@ -82,7 +82,7 @@ __device__ __forceinline__ void store8(void* p, int64_t e, float (&v)[8]) {
 // quotient in 64 bits decides: with 24-bit t and m, a quotient of at least a
 // quarter that is not exactly k + 1/2 is at least 2^-35 from it, and the
 // 53-bit rounding (2^-47 below 128) cannot reach or cross it.
-__device__ __forceinline__ int exact_code(float t, float m) {
+__device__ __noinline__ int exact_code(float t, float m) {
   return m > 0.f ? __double2int_rn(127.0 * static_cast<double>(t) / static_cast<double>(m)) : 0;
 }
 
@@ -100,7 +100,7 @@ __device__ __forceinline__ uint2 codes8(const float (&t)[8], float m, float f) {
     far = fmaxf(far, fabsf(p - __fsub_rn(r, kRoundMagic)));
   }
   if (!(far < 0.49996f) || !(m > 1.0e-30f)) {   // tiny m: f may be infinite
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(exact_code(t[i], m));
   }
   const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
@@ -123,39 +123,33 @@ rmsnorm_quant_kernel(const void* x, const void* res, const void* __restrict__ we
 
   float t[NV][8];
   float ss = 0.f, m = 0.f;
+  {
+    float r[RES ? NV : 1][8];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = tid + j * T;
-    if (c < chunks) load8<BF16>(x, e0 + 8 * c, t[j]);
-  }
-  if constexpr (RES) {
-    float r[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j) {            // every load first
       const int c = tid + j * T;
-      if (c < chunks) load8<BF16>(res, e0 + 8 * c, r[j]);
+      if (c < chunks) {
+        load8<BF16>(x, e0 + 8 * c, t[j]);
+        if constexpr (RES) load8<BF16>(res, e0 + 8 * c, r[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = tid + j * T;
       if (c < chunks) {
+        if constexpr (RES) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[j][i] = __fadd_rn(t[j][i], r[j][i]);
-        store8<BF16>(stream_out, e0 + 8 * c, t[j]);
-      }
-    }
-  }
+          for (int i = 0; i < 8; ++i) t[j][i] = __fadd_rn(t[j][i], r[j][i]);
+          store8<BF16>(stream_out, e0 + 8 * c, t[j]);
+        }
+        float w[8];
+        load8_weight<BF16>(weight, 8 * c, w);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = tid + j * T;
-    if (c < chunks) {
-      float w[8];
-      load8_weight<BF16>(weight, 8 * c, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(t[j][i], t[j][i], ss);
-        t[j][i] = __fmul_rn(t[j][i], w[i]);
-        m = fmaxf(m, fabsf(t[j][i]));
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(t[j][i], t[j][i], ss);
+          t[j][i] = __fmul_rn(t[j][i], w[i]);
+          m = fmaxf(m, fabsf(t[j][i]));
+        }
       }
     }
   }
