@@ -155,13 +155,13 @@ struct AttnArgs {
   const int32_t* table;      // [batch][max_pages]
   const int32_t* lengths;    // [batch]
   uint16_t* out;             // [batch][q_len][heads][D]
-  float* part_o;             // [splits][batch * q_len * heads][D] (splits > 1)
-  float2* part_ml;           // [splits][batch * q_len * heads]
+  float* part_o;             // [split][unit][rows of a tile][D] (splits > 1)
+  float2* part_ml;           // [split][unit][rows of a tile]: maximum, sum
   int64_t num_pages;
-  int64_t out_rows;          // batch * q_len * heads
   int max_pages, page_size;
   int q_len, kv_heads, ratio;   // heads = kv_heads * ratio
-  int row_tiles, splits;
+  int row_tiles;
+  int units, splits;
   int rotate;
   float norm;                // fp32(1 / sqrt(D))
   float scale_log2;          // scale * log2(e)
@@ -169,23 +169,31 @@ struct AttnArgs {
 
 constexpr int kWarps = 4;
 
+// A step is two tiles: 32 positions whose products, maximum and exponentials
+// interleave.
 template <int D, int GROUP, int NT, int STAGES>
 struct Cfg {
   static constexpr int G = D / GROUP;
   static constexpr int CODE_BYTES = 16 * D / 2;             // one tile's codes of K or V
   static constexpr int SCALE_BYTES = 16 * G * 2;
-  static constexpr int STAGE_BYTES = 2 * CODE_BYTES + 2 * SCALE_BYTES;
+  static constexpr int STAGE_BYTES = 4 * (CODE_BYTES + SCALE_BYTES);   // K0 K1 V0 V1, then their scales
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;   // per warp
   static constexpr int ROWS = 8 * NT;
   static constexpr int JOIN_STRIDE = D + 4;                 // floats per row of a warp's partial output
   static constexpr int JOIN_BYTES = kWarps * ROWS * (JOIN_STRIDE + 2) * 4;
   static constexpr int MAIN_BYTES = kWarps * RING_BYTES;
   static constexpr int BUF_BYTES = MAIN_BYTES > JOIN_BYTES ? MAIN_BYTES : JOIN_BYTES;
-  static constexpr int SMEM_BYTES = BUF_BYTES + kWarps * STAGES * 4;   // + valid positions per tile in flight
+  static constexpr int Q_AT = BUF_BYTES;                    // query rows as operands, and the warps' maxima
+  static constexpr int Q_BYTES = ROWS * D * 2;
+  static constexpr int VALID_AT = Q_AT + Q_BYTES + 16;      // valid positions of the tiles in flight
+  static constexpr int SMEM_BYTES = VALID_AT + kWarps * STAGES * 8;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -198,6 +206,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same of bytes, 32 deep: signed K times signed or unsigned digits of q.
+template <bool SIGNED>
+__device__ __forceinline__ void mma16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (SIGNED)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -223,24 +247,31 @@ __device__ __forceinline__ __half2 bits_h2(uint32_t w) { return *reinterpret_cas
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return h2_bits(__floats2half2_rn(lo, hi)); }
 
-// The codes of nibbles 0, 1, 2, 3 of both halves of w as fp16 pairs.  Under
-// 0x6400 (1024, unit steps) nibble n reads 1024 + (n ^ 8) = 1032 + code; one
-// nibble further up the steps are 16: 1024 + 16 (code + 8) = 1152 + 16 code.
+// Nibbles 0, 1, 2, 3 of both halves of w as fp16 pairs, without arithmetic: the
+// low bits of an fp16 number with a zero exponent are a subnormal, which the
+// products take exactly.  x[0], x[2]: (code + 8) 2^-24; x[1], x[3]: 16 times
+// that.
+__device__ __forceinline__ uint32_t mask_flip(uint32_t w, uint32_t mask, uint32_t flip) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(mask), "r"(flip));   // (w & mask) ^ flip
+  return r;
+}
 __device__ __forceinline__ void unpack4(uint32_t w, uint32_t (&x)[4]) {
-  const __half2 k1032 = bits_h2(0x64086408u), k16th = bits_h2(0x2C002C00u), km72 = bits_h2(0xD480D480u);
   const uint32_t u = w >> 8;
-  x[0] = h2_bits(__hsub2(bits_h2((w & 0x000F000Fu) ^ 0x64086408u), k1032));
-  x[1] = h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) ^ 0x64806480u), k16th, km72));
-  x[2] = h2_bits(__hsub2(bits_h2((u & 0x000F000Fu) ^ 0x64086408u), k1032));
-  x[3] = h2_bits(__hfma2(bits_h2((u & 0x00F000F0u) ^ 0x64806480u), k16th, km72));
+  x[0] = mask_flip(w, 0x000F000Fu, 0x00080008u);
+  x[1] = mask_flip(w, 0x00F000F0u, 0x00800080u);
+  x[2] = mask_flip(u, 0x000F000Fu, 0x00080008u);
+  x[3] = mask_flip(u, 0x00F000F0u, 0x00800080u);
 }
 
 // Byte offset of 16-byte chunk `ch` of position t in a tile's codes.  The XOR
-// spreads the chunks that one load instruction reads over the banks: K is read
-// chunk by chunk for positions 0..7 at once, V for four positions at once.
-template <int D>
+// spreads the chunks that one load instruction reads over the banks: K with
+// one scale a row is read 16 (or 8) bytes a lane and needs none; with more
+// scales chunk by chunk for positions 0..7 at once, V for four at once.
+template <int D, int G>
 __device__ __forceinline__ int k_chunk(int t, int ch) {
-  if constexpr (D == 128) return t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
+  if constexpr (G == 1) return t * (D / 2) + (ch << 4);
+  else if constexpr (D == 128) return t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
   else return t * 32 + ((ch ^ ((t >> 2) & 1)) << 4);
 }
 template <int D>
@@ -249,82 +280,108 @@ __device__ __forceinline__ int v_chunk(int t, int ch) {
   else return t * 32 + (ch << 4);
 }
 
+__device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
+  const int n = a.lengths[b], most = a.max_pages * a.page_size;
+  return n < 0 ? 0 : n > most ? most : n;
+}
+
+// Division of the work.  A unit is a (sequence, K/V head, tile of query rows);
+// CTA (unit, split) takes the split's equal part of the sequence's steps.  With
+// more than one split the parts' sums go to the workspace, and kv4_join_kernel
+// adds them in order.
 template <int D, int GROUP, int NT, int STAGES>
-__global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<D, GROUP, NT, STAGES>;
   constexpr int G = C::G;
   constexpr int NG = D / 32;                  // words of a row that one lane reads of K
   constexpr int MT = D / 16;                  // 16-element tiles of the output
   constexpr int TPG = GROUP / 16;             // of them in a scale group
+  constexpr int TILE_SCALES = 32 * G;         // bytes of a tile's scales
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * C::RING_BYTES;
-  int* nvalid = reinterpret_cast<int*>(smem + C::BUF_BYTES) + warp * STAGES;
+  int2* nvalid = reinterpret_cast<int2*>(smem + C::VALID_AT) + warp * STAGES;
 
   grid_dependency_sync();
-  const int unit = blockIdx.x, split = blockIdx.y;
-  const int rt = unit % a.row_tiles;
-  const int bh = unit / a.row_tiles;
-  const int h = bh % a.kv_heads, b = bh / a.kv_heads;
   const int rows = a.q_len * a.ratio;
-  const int capacity = a.max_pages * a.page_size;
-  int len = a.lengths[b];
-  if (len < 0 || len > capacity) {
-    if (threadIdx.x == 0) atomicOr(&hadq_kv4_fault, kFaultLength);
-    len = len < 0 ? 0 : capacity;
+  const int unit = blockIdx.x, split = blockIdx.y;
+  const int rt = unit % a.row_tiles, h = unit / a.row_tiles % a.kv_heads, b = unit / a.row_tiles / a.kv_heads;
+  const int len = length_of(a, b);
+  if (threadIdx.x == 0 && len != a.lengths[b]) atomicOr(&hadq_kv4_fault, kFaultLength);
+  const int64_t part = (static_cast<int64_t>(split) * a.units + unit) * C::ROWS;   // first row in the workspace
+  const int steps = (len + 31) >> 5, per = (steps + a.splits - 1) / a.splits;
+  const int t0 = min(split * per, steps), count = min(per, steps - t0);
+  if (a.splits > 1 && count == 0) {             // nothing here: no part (the join skips sums of 0)
+    if (threadIdx.x < C::ROWS) a.part_ml[part + threadIdx.x] = make_float2(-1.0e30f, 0.f);
+    return;
   }
+  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;   // steps, interleaved over the warps
 
-  // tiles of this split, interleaved over the warps
-  const int tiles = (len + 15) >> 4;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int t0 = min(split * per, tiles), t1 = min(t0 + per, tiles);
-  const int mine = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
-
-  // ---- page entries of the warp's next 32 tiles, one per lane
-  int ent_page = -1, ent_off = 0;
+  // ---- copies.  Lane l holds the entry of tile l & 1 of the warp's step
+  // i0 + l / 2: the number of the 16-position run in the cache (fewer than
+  // 2^32: a run takes 512 bytes or more), or kNoTile for a page outside it.
+  constexpr uint32_t kNoTile = 0xFFFFFFFFu;
+  uint32_t entry = kNoTile;
   const int blocks = a.page_size >> 4;
   auto load_entries = [&](int i0) {
-    const int i = i0 + lane;
-    ent_page = -1;
-    if (i < mine) {
-      const int tile = t0 + warp + i * kWarps;
+    const int tile = (t0 + warp + (i0 + (lane >> 1)) * kWarps) * 2 + (lane & 1);
+    entry = kNoTile;
+    if (tile * 16 < len) {
       const int p = tile / blocks;
-      ent_off = (tile - p * blocks) << 4;
-      ent_page = a.table[static_cast<int64_t>(b) * a.max_pages + p];
-      if (ent_page < 0 || ent_page >= a.num_pages) {
-        atomicOr(&hadq_kv4_fault, kFaultPage);
-        ent_page = -1;
-      }
+      const int page = a.table[static_cast<int64_t>(b) * a.max_pages + p];
+      if (page < 0 || page >= a.num_pages) atomicOr(&hadq_kv4_fault, kFaultPage);
+      else entry = (static_cast<uint32_t>(page) * a.kv_heads + h) * blocks + (tile - p * blocks);
     }
   };
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  // this lane's 16-byte chunks: of codes, `lane` and (D = 128) lane + 32 of a
+  // tile; of scales, chunk lane & 7 of K (lane bit 3: V) of tile lane / 16
+  const uint8_t* k_lane = a.k_codes + 16 * lane;
+  const uint8_t* v_lane = a.v_codes + 16 * lane;
+  const uint8_t* s_lane = reinterpret_cast<const uint8_t*>((lane & 8) ? a.v_scales : a.k_scales) + 16 * (lane & 7);
+  const bool s_live = (lane & 7) < 2 * G;
+  const uint32_t s_dst = ring_u + 4 * C::CODE_BYTES + ((lane >> 4) + ((lane & 8) ? 2 : 0)) * C::SCALE_BYTES + 16 * (lane & 7);
+  uint32_t k_dst[D / 64], v_dst[D / 64];
+#pragma unroll
+  for (int u = 0; u < D / 64; ++u) {
+    const int j = lane + 32 * u;
+    k_dst[u] = ring_u + k_chunk<D, G>(j / NG, j % NG);
+    v_dst[u] = ring_u + 2 * C::CODE_BYTES + v_chunk<D>(j / NG, j % NG);
+  }
   auto issue = [&](int i) {
     if (i < mine) {
-      if ((i & 31) == 0) load_entries(i);
-      const int page = __shfl_sync(0xffffffffu, ent_page, i & 31);
-      const int off = __shfl_sync(0xffffffffu, ent_off, i & 31);
-      const int st = i % STAGES;
-      const int tile = t0 + warp + i * kWarps;
-      // a page outside the cache: nothing is read, its positions are masked
-      const int nv = page < 0 ? 0 : min(16, len - tile * 16);
-      if (lane == 0) nvalid[st] = nv;
-      const int64_t cell = (static_cast<int64_t>(page < 0 ? 0 : page) * a.kv_heads + h) * a.page_size + (page < 0 ? 0 : off);
-      const uint8_t* kc = a.k_codes + cell * (D / 2);
-      const uint8_t* vc = a.v_codes + cell * (D / 2);
-      const uint32_t dst = ring_u + st * C::STAGE_BYTES;
+      if ((i & 15) == 0) load_entries(i);
+      const uint32_t e0 = __shfl_sync(0xffffffffu, entry, (i & 15) * 2), e1 = __shfl_sync(0xffffffffu, entry, (i & 15) * 2 + 1);
+      const uint32_t st = (i % STAGES) * C::STAGE_BYTES;
+      const int left = len - (t0 + warp + i * kWarps) * 32;
+      const uint32_t es = lane < 16 ? e0 : e1;
+      if (left >= 32 && e0 != kNoTile && e1 != kNoTile) {
+        if (lane == 0) nvalid[i % STAGES] = make_int2(16, 16);
 #pragma unroll
-      for (int u = 0; u < D / 64; ++u) {
-        const int j = lane + 32 * u, t = j / NG, ch = j % NG;
-        const int bytes = t < nv ? 16 : 0;
-        cp_async16(dst + k_chunk<D>(t, ch), kc + 16 * j, bytes);
-        cp_async16(dst + C::CODE_BYTES + v_chunk<D>(t, ch), vc + 16 * j, bytes);
-      }
-      const int j = lane & 15;
-      if (j < 2 * G) {                        // scales: lanes 0.. of K, 16.. of V
-        const int bytes = min(max(nv * 2 * G - 16 * j, 0), 16);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>((lane < 16 ? a.k_scales : a.v_scales) + cell * G) + 16 * j;
-        cp_async16(dst + 2 * C::CODE_BYTES + (lane < 16 ? 0 : C::SCALE_BYTES) + 16 * j, src, bytes);
+        for (int u = 0; u < D / 64; ++u) {
+          cp_async16(st + k_dst[u], k_lane + static_cast<uint64_t>(e0) * C::CODE_BYTES + 512 * u);
+          cp_async16(st + k_dst[u] + C::CODE_BYTES, k_lane + static_cast<uint64_t>(e1) * C::CODE_BYTES + 512 * u);
+          cp_async16(st + v_dst[u], v_lane + static_cast<uint64_t>(e0) * C::CODE_BYTES + 512 * u);
+          cp_async16(st + v_dst[u] + C::CODE_BYTES, v_lane + static_cast<uint64_t>(e1) * C::CODE_BYTES + 512 * u);
+        }
+        if (s_live) cp_async16(st + s_dst, s_lane + static_cast<uint64_t>(es) * TILE_SCALES);
+      } else {
+        // the end of a sequence, or a page outside the cache: zeros in place
+        // of what must not be read, and masked below
+        const int n0 = e0 == kNoTile ? 0 : min(16, left), n1 = e1 == kNoTile ? 0 : min(16, max(left - 16, 0));
+        if (lane == 0) nvalid[i % STAGES] = make_int2(n0, n1);
+        const uint64_t f0 = e0 == kNoTile ? 0 : e0, f1 = e1 == kNoTile ? 0 : e1;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          const int t = (lane + 32 * u) / NG, b0 = t < n0 ? 16 : 0, b1 = t < n1 ? 16 : 0;
+          cp_async16(st + k_dst[u], k_lane + f0 * C::CODE_BYTES + 512 * u, b0);
+          cp_async16(st + k_dst[u] + C::CODE_BYTES, k_lane + f1 * C::CODE_BYTES + 512 * u, b1);
+          cp_async16(st + v_dst[u], v_lane + f0 * C::CODE_BYTES + 512 * u, b0);
+          cp_async16(st + v_dst[u] + C::CODE_BYTES, v_lane + f1 * C::CODE_BYTES + 512 * u, b1);
+        }
+        const int bytes = min(max((lane < 16 ? n0 : n1) * 2 * G - 16 * (lane & 7), 0), 16);
+        if (s_live) cp_async16(st + s_dst, s_lane + (lane < 16 ? f0 : f1) * TILE_SCALES, bytes);
       }
     }
     cp_async_commit();
@@ -332,54 +389,100 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue(i);
 
-  // ---- query rows: lane (r, c) holds elements 32 g + 8 c + 0..7 of row r
+  // ---- query rows.  A lane's words of a K row, w = 0 .. NG - 1: with one scale
+  // per row elements c D / 4 + 8 w .. (consecutive: one load), else 32 w + 8 c ..
+  // (every word in a group of its own).  D / 8 lanes rotate a row, 8 elements
+  // each, and leave it in the order in which lane (r, c) takes row r.
+  constexpr int LPR = D / 8, PASS = kWarps * 32 / LPR;        // rows of a pass of all warps
+  constexpr int PASSES = (C::ROWS + PASS - 1) / PASS;
+  uint4* qs = reinterpret_cast<uint4*>(smem + C::Q_AT);       // [row / 8][word][lane]
+  float* tops = reinterpret_cast<float*>(smem + C::Q_AT + C::Q_BYTES);
+  float v[PASSES][8], f = a.scale_log2;
+  if (a.rotate) f *= a.norm;
+#pragma unroll
+  for (int ps = 0; ps < PASSES; ++ps) {
+    const int row = ps * PASS + threadIdx.x / LPR, rho = rt * C::ROWS + row, part8 = threadIdx.x % LPR;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (row < C::ROWS && rho < rows) {
+      const int i = rho / a.ratio, head = h * a.ratio + rho - i * a.ratio;
+      w = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride + static_cast<int64_t>(head) * D + 8 * part8);
+    }
+    unpack_bf16x2(w.x, v[ps][0], v[ps][1]);
+    unpack_bf16x2(w.y, v[ps][2], v[ps][3]);
+    unpack_bf16x2(w.z, v[ps][4], v[ps][5]);
+    unpack_bf16x2(w.w, v[ps][6], v[ps][7]);
+    if (a.rotate) {
+      fwht_bits<8, 0, 3>(v[ps]);
+#pragma unroll
+      for (int s = 1; s < LPR; s <<= 1) {
+        const float sgn = (part8 & s) ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[ps][i] = fmaf(v[ps][i], sgn, __shfl_xor_sync(0xffffffffu, v[ps][i], s));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[ps][i] *= f;
+  }
+  float mx = 0.f;
+#pragma unroll
+  for (int ps = 0; ps < PASSES; ++ps) mx = fmaxf(mx, absmax_regs(v[ps], 0, 8));
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  if (lane == 0) tops[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, tops[w]);
+  const int eb = min(max(static_cast<int>(__float_as_uint(mx) >> 23), 16), 220);
+  const float ulp = __uint_as_float(static_cast<uint32_t>(eb) << 23);        // 2^e <= the tile's largest < 2^(e + 1)
+  const float down = __uint_as_float(static_cast<uint32_t>(254 - eb) << 23);
+  const float kf = G == 1 ? ulp * (1.f / 262144.f) : ulp * 16777216.f;
+#pragma unroll
+  for (int ps = 0; ps < PASSES; ++ps) {
+    const int row = ps * PASS + threadIdx.x / LPR, part8 = threadIdx.x % LPR;
+    const int w = G == 1 ? part8 % NG : part8 / 4, qc = G == 1 ? part8 / NG : part8 % 4;
+    uint4 x;
+    if constexpr (G == 1) {
+      // digits of round(q 2^14 / 2^e) = 256 high + low: even elements' high
+      // ones, odd ones', then the low ones
+      uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = min(max(__float2int_rn(v[ps][i] * down * 16384.f), -32768), 32767);
+        hi[i & 1] |= (static_cast<uint32_t>(q >> 8) & 255u) << (8 * (i >> 1));
+        lo[i & 1] |= (static_cast<uint32_t>(q) & 255u) << (8 * (i >> 1));
+      }
+      x = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+    } else {
+      // fp16 pairs, in the units of K's nibbles
+      x.x = pack_half2(v[ps][0] * down, v[ps][4] * down);
+      x.y = pack_half2(v[ps][1] * (down * 0.0625f), v[ps][5] * (down * 0.0625f));
+      x.z = pack_half2(v[ps][2] * down, v[ps][6] * down);
+      x.w = pack_half2(v[ps][3] * (down * 0.0625f), v[ps][7] * (down * 0.0625f));
+    }
+    if (row < C::ROWS) qs[((row >> 3) * NG + w) * 32 + (row & 7) * 4 + qc] = x;
+  }
+  __syncthreads();
   uint32_t qb[NT][NG][4];
-  float qf[NT][2];                            // factor of rows 2c, 2c + 1 to base-2 scores
-  int limit[NT][2];                           // first position that the row does not see
+  float bias[NT][G][4];                       // G > 1: what the 8 in (code + 8) adds to a row's sums, negative
+  int limit[NT][2];                           // first position that rows 2c, 2c + 1 do not see
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int rho = rt * C::ROWS + nt * 8 + r;
-    float v[D / 4];
-    if (rho < rows) {
-      const int i = rho / a.ratio;
-      const int head = h * a.ratio + rho - i * a.ratio;
-      const uint16_t* p = a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride + static_cast<int64_t>(head) * D + 8 * c;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p + 32 * g);
-        unpack_bf16x2(w.x, v[8 * g + 0], v[8 * g + 1]);
-        unpack_bf16x2(w.y, v[8 * g + 2], v[8 * g + 3]);
-        unpack_bf16x2(w.z, v[8 * g + 4], v[8 * g + 5]);
-        unpack_bf16x2(w.w, v[8 * g + 6], v[8 * g + 7]);
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bias[nt][g][k] = 0.f;
+#pragma unroll
+      for (int w = g * (GROUP / 32); w < (g + 1) * (GROUP / 32); ++w) {
+        const uint4 x = qs[(nt * NG + w) * 32 + lane];
+        qb[nt][w][0] = x.x, qb[nt][w][1] = x.y, qb[nt][w][2] = x.z, qb[nt][w][3] = x.w;
+        if constexpr (G > 1) {
+          mma16816(bias[nt][g], 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.x, x.y);
+          mma16816(bias[nt][g], 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.z, x.w);
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) v[i] = 0.f;
     }
-    if (a.rotate) {
-      fwht_bits<D / 4, 0, (D == 128 ? 5 : 4)>(v);
-#pragma unroll
-      for (int s = 1; s < 4; s <<= 1) {
-        const float sgn = (c & s) ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i) v[i] = fmaf(v[i], sgn, __shfl_xor_sync(0xffffffffu, v[i], s));
-      }
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) v[i] *= a.norm;
-    }
-    float mx = absmax_regs(v, 0, D / 4);
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const int eb = min(max(static_cast<int>(__float_as_uint(mx) >> 23), 1), 253);
-    const float down = __uint_as_float(static_cast<uint32_t>(254 - eb) << 23);   // 2^-e: the largest in [1, 2)
-    const float up = __uint_as_float(static_cast<uint32_t>(eb) << 23) * a.scale_log2;
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) qb[nt][g][j] = pack_half2(v[8 * g + j] * down, v[8 * g + j + 4] * down);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      qf[nt][e] = __shfl_sync(0xffffffffu, up, (2 * c + e) * 4);
       const int col = rt * C::ROWS + nt * 8 + 2 * c + e;
       limit[nt][e] = len - a.q_len + 1 + (col < rows ? col / a.ratio : 0);
     }
@@ -387,6 +490,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid
 
   float o[MT][NT][4];
   float m[NT][2], l[NT][2];
+  float ones[NT][4];                          // G == 1: 8 times P's sums, in the units of even and odd nibbles
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -396,90 +500,192 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m[nt][e] = -1.0e30f, l[nt][e] = 0.f;
+    for (int e = 0; e < 2; ++e) m[nt][e] = -1.0e30f, l[nt][e] = 0.f, ones[nt][e] = ones[nt][2 + e] = 0.f;
 
-  // Row i of a tile's products is position pi(i): pi(2c) = c, pi(2c + 1) = 4 + c,
-  // pi(2c + 8) = 8 + c, pi(2c + 9) = 12 + c, so the four lanes c read four
-  // neighbouring positions of V.
-  const int pr = (r & 1) * 4 + (r >> 1);      // pi(r); pi(r + 8) = pr + 8
+  // positions below this are seen by every row of the tile
+  const int seen_by_all = len - a.q_len + 1 + (rt * C::ROWS) / a.ratio;
 
+  // Row i of a tile's products is position pi(i): pi(2c) = c, pi(2c + 1) = 4 +
+  // (c ^ 1), pi(i + 8) = pi(i) + 8.  The four lanes c then read four
+  // neighbouring positions of V at a time, and lanes r, r + 1 positions of K
+  // that differ in their lowest bit (different banks).
+  const int pr = (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1;   // pi(r)
+  int k_at[G == 1 ? 1 : NG], v_at[G][2];      // this lane's words in a tile
+  if constexpr (G == 1) {
+    k_at[0] = pr * (D / 2) + c * (D / 8);
+  } else {
+#pragma unroll
+    for (int w = 0; w < NG; ++w) k_at[w] = k_chunk<D, G>(pr, w) + 4 * c;
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = e ? 4 + (c ^ 1) : c;
+      if constexpr (GROUP == 128) v_at[g][e] = v_chunk<D>(t, r >> 1) + (r & 1) * 8;
+      else if constexpr (GROUP == 64) v_at[g][e] = v_chunk<D>(t, 2 * g + (r >> 2)) + (r & 3) * 4;
+      else v_at[g][e] = v_chunk<D>(t, g) + r * 2;
+    }
+
+#pragma unroll 1
   for (int i = 0; i < mine; ++i) {
     cp_async_wait<STAGES - 2>();
     __syncwarp();
     issue(i + STAGES - 1);                    // into the stage consumed in the last round
-    const int st = i % STAGES;
-    const uint8_t* kt = ring + st * C::STAGE_BYTES;
-    const uint8_t* vt = kt + C::CODE_BYTES;
-    const __half* kst = reinterpret_cast<const __half*>(kt + 2 * C::CODE_BYTES);
-    const __half* vst = kst + 16 * G;
-    const int nv = nvalid[st];
-    const int pos = (t0 + warp + i * kWarps) * 16 + pr;
+    const uint8_t* kt = ring + (i % STAGES) * C::STAGE_BYTES;
+    const uint8_t* vt = kt + 2 * C::CODE_BYTES;
+    const __half* kst = reinterpret_cast<const __half*>(kt + 4 * C::CODE_BYTES) + pr * G;
+    const __half* vst = kst + 32 * G;
+    const int2 nv = nvalid[i % STAGES];
+    const int pos = (t0 + warp + i * kWarps) * 32;
 
-    // ---- S^T = K q^T, K's scales applied to the sums of each group
-    float s[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[nt][k] = 0.f;
+    // ---- S^T = K q^T: s times kk are the base-2 scores
+    float s[2][NT][4], kk[2][2];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      float acc[NT][4];
+      float acc[2][NT][4];
+      uint32_t kw[2][2][GROUP / 32];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t* at = kt + tt * C::CODE_BYTES + e * (C::CODE_BYTES / 2);
+          if constexpr (G == 1 && D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + k_at[0]);
+            kw[tt][e][0] = x.x, kw[tt][e][1] = x.y, kw[tt][e][2] = x.z, kw[tt][e][3] = x.w;
+          } else if constexpr (G == 1) {
+            const uint2 x = *reinterpret_cast<const uint2*>(at + k_at[0]);
+            kw[tt][e][0] = x.x, kw[tt][e][1] = x.y;
+          } else {
 #pragma unroll
-      for (int w = g * (GROUP / 32); w < (g + 1) * (GROUP / 32); ++w) {
-        uint32_t xa[4], xb[4];
-        unpack4(*reinterpret_cast<const uint32_t*>(kt + k_chunk<D>(pr, w) + 4 * c), xa);
-        unpack4(*reinterpret_cast<const uint32_t*>(kt + k_chunk<D>(pr + 8, w) + 4 * c), xb);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(acc[nt], xa[0], xb[0], xa[1], xb[1], qb[nt][w][0], qb[nt][w][1]);
-          mma16816(acc[nt], xa[2], xb[2], xa[3], xb[3], qb[nt][w][2], qb[nt][w][3]);
+            for (int w = 0; w < GROUP / 32; ++w) kw[tt][e][w] = *reinterpret_cast<const uint32_t*>(at + k_at[g * (GROUP / 32) + w]);
+          }
         }
-      }
-      const float k0 = __half2float(kst[pr * G + g]), k1 = __half2float(kst[(pr + 8) * G + g]);
+      if constexpr (G == 1) {
+        int high[2][NT][4], low[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        s[nt][0] = fmaf(acc[nt][0], k0, s[nt][0]);
-        s[nt][1] = fmaf(acc[nt][1], k0, s[nt][1]);
-        s[nt][2] = fmaf(acc[nt][2], k1, s[nt][2]);
-        s[nt][3] = fmaf(acc[nt][3], k1, s[nt][3]);
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) high[tt][nt][k] = low[tt][nt][k] = 0;
+#pragma unroll
+        for (int w = 0; w < NG; ++w)
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) {
+            // a nibble in the upper half of a byte is the signed byte 16 code
+            const uint32_t a0 = (kw[tt][0][w] << 4) & 0xF0F0F0F0u, a2 = kw[tt][0][w] & 0xF0F0F0F0u;
+            const uint32_t a1 = (kw[tt][1][w] << 4) & 0xF0F0F0F0u, a3 = kw[tt][1][w] & 0xF0F0F0F0u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16832<true>(high[tt][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
+              mma16832<false>(low[tt][nt], a0, a1, a2, a3, qb[nt][w][2], qb[nt][w][3]);
+            }
+          }
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[tt][nt][k] = __int2float_rn(high[tt][nt][k] * 256 + low[tt][nt][k]);
+      } else {
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[tt][nt][k] = bias[nt][g][k];
+#pragma unroll
+        for (int w = 0; w < GROUP / 32; ++w)
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) {
+            uint32_t xa[4], xb[4];
+            unpack4(kw[tt][0][w], xa);
+            unpack4(kw[tt][1][w], xb);
+            const int gw = g * (GROUP / 32) + w;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(acc[tt][nt], xa[0], xb[0], xa[1], xb[1], qb[nt][gw][0], qb[nt][gw][1]);
+              mma16816(acc[tt][nt], xa[2], xb[2], xa[3], xb[3], qb[nt][gw][2], qb[nt][gw][3]);
+            }
+          }
+      }
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        float k2[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          k2[e] = __half2float(kst[tt * 16 * G + 8 * e * G + g]) * kf;
+          kk[tt][e] = G == 1 ? k2[e] : 1.f;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            s[tt][nt][k] = G == 1 ? acc[tt][nt][k]
+                           : g == 0 ? acc[tt][nt][k] * k2[k >> 1]
+                                    : fmaf(acc[tt][nt][k], k2[k >> 1], s[tt][nt][k]);
       }
     }
-    // V's scales of positions pr, pr + 8, and log2 of the largest of a position
-    float sv[2][G], lv[2];
+    // V's scales of this lane's four positions, and log2 of the largest of each
+    float sv[2][2][G], lv[2][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float top = 0.f;
+    for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        // finite, so that a position that a row does not see adds 0 whatever its scale
-        sv[e][g] = fminf(fmaxf(__half2float(vst[(pr + 8 * e) * G + g]), -65504.f), 65504.f);
-        top = fmaxf(top, fabsf(sv[e][g]));
-      }
-      lv[e] = log2_fast(fmaxf(top, 5.9604645e-8f));     // at least the least fp16 above zero
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int g = 0; g < G; ++g) sv[tt][e][g] = __half2float(vst[tt * 16 * G + 8 * e * G + g]);
+    const bool masked = nv.x + nv.y < 32 || pos + 32 > seen_by_all;
+    if (masked) {
+      // finite scales, so that a position that a row does not see adds 0 whatever lies there
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < G; ++g) sv[tt][e][g] = fminf(fmaxf(sv[tt][e][g], -65504.f), 65504.f);
     }
-    const bool seen0 = pr < nv, seen1 = pr + 8 < nv;
-    bool rise = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        s[nt][e] = seen0 && pos < limit[nt][e] ? s[nt][e] * qf[nt][e] : -INFINITY;
-        s[nt][2 + e] = seen1 && pos + 8 < limit[nt][e] ? s[nt][2 + e] * qf[nt][e] : -INFINITY;
-        rise |= s[nt][e] + lv[0] > m[nt][e] + 8.f || s[nt][2 + e] + lv[1] > m[nt][e] + 8.f;
+        float top = fabsf(sv[tt][e][0]);
+#pragma unroll
+        for (int g = 1; g < G; ++g) top = fmaxf(top, fabsf(sv[tt][e][g]));
+        lv[tt][e] = fmaxf(log2_fast(top), -24.f);          // the least fp16 above zero is 2^-24
+      }
+    if (masked) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = pr + 8 * (k >> 1);
+          const bool there = at < (tt ? nv.y : nv.x);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            s[tt][nt][k] = there && pos + 16 * tt + at < limit[nt][k & 1] ? s[tt][nt][k] * kk[tt][k >> 1] : -INFINITY;
+        }
+        kk[tt][0] = kk[tt][1] = 1.f;
       }
     }
     // The running maximum moves only when a value passes it by 2^8: P stays
-    // below 2^8, and most tiles need one vote instead of the exchange.
+    // below 2^8, and most steps need one vote instead of the exchange.
+    float up[NT][2];
+    bool rise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        up[nt][e] = fmaxf(fmaxf(fmaf(s[0][nt][e], kk[0][0], lv[0][0]), fmaf(s[0][nt][2 + e], kk[0][1], lv[0][1])),
+                          fmaxf(fmaf(s[1][nt][e], kk[1][0], lv[1][0]), fmaf(s[1][nt][2 + e], kk[1][1], lv[1][1])));
+        rise |= up[nt][e] > m[nt][e] + 8.f;
+      }
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[nt][e] + lv[0], s[nt][2 + e] + lv[1]);
+          float t = up[nt][e];
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -487,6 +693,8 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid
           const float f = exp2_fast(m[nt][e] - t);
           m[nt][e] = t;
           l[nt][e] *= f;
+          ones[nt][e] *= f;
+          ones[nt][2 + e] *= f;
 #pragma unroll
           for (int k = 0; k < MT; ++k) {
             o[k][nt][e] *= f;
@@ -498,47 +706,78 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        s[nt][e] = exp2_fast(s[nt][e] - m[nt][e]);
-        s[nt][2 + e] = exp2_fast(s[nt][2 + e] - m[nt][e]);
-        l[nt][e] += s[nt][e] + s[nt][2 + e];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+          s[tt][nt][e] = exp2_fast(fmaf(s[tt][nt][e], kk[tt][0], -m[nt][e]));
+          s[tt][nt][2 + e] = exp2_fast(fmaf(s[tt][nt][2 + e], kk[tt][1], -m[nt][e]));
+        }
+        l[nt][e] += (s[0][nt][e] + s[0][nt][2 + e]) + (s[1][nt][e] + s[1][nt][2 + e]);
       }
 
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      uint32_t pb[NT][2];
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        pb[nt][0] = transpose8x8(pack_half2(s[nt][0] * sv[0][g], s[nt][1] * sv[0][g]));
-        pb[nt][1] = transpose8x8(pack_half2(s[nt][2] * sv[1][g], s[nt][3] * sv[1][g]));
-      }
-      // lane (r, c): elements g GROUP + r GROUP / 8 + 0..GROUP / 8 - 1 of positions c, 4 + c, 8 + c, 12 + c
-      uint32_t w[4][2];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int p = 4 * t + c;
-        if constexpr (GROUP == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(vt + v_chunk<D>(p, r >> 1) + (r & 1) * 8);
-          w[t][0] = x.x;
-          w[t][1] = x.y;
-        } else if constexpr (GROUP == 64) {
-          w[t][0] = *reinterpret_cast<const uint32_t*>(vt + v_chunk<D>(p, 2 * g + (r >> 2)) + (r & 3) * 4);
-        } else {
-          w[t][0] = *reinterpret_cast<const uint16_t*>(vt + v_chunk<D>(p, g) + r * 2);
-        }
-      }
-#pragma unroll
-      for (int q4 = 0; q4 < TPG / 2; ++q4) {      // four nibbles, two tiles at a time
-        const uint32_t sel = (q4 & 1) ? 0x7632u : 0x5410u;
-        uint32_t xa[4], xb[4];
-        unpack4(__byte_perm(w[0][q4 >> 1], w[1][q4 >> 1], sel), xa);
-        unpack4(__byte_perm(w[2][q4 >> 1], w[3][q4 >> 1], sel), xb);
+      for (int tt = 0; tt < 2; ++tt) {
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma16816(o[g * TPG + 2 * q4][nt], xa[0], xa[1], xb[0], xb[1], pb[nt][0], pb[nt][1]);
-          mma16816(o[g * TPG + 2 * q4 + 1][nt], xa[2], xa[3], xb[2], xb[3], pb[nt][0], pb[nt][1]);
+          pb[nt][0] = transpose8x8(pack_half2(s[tt][nt][0] * sv[tt][0][g], s[tt][nt][1] * sv[tt][0][g]));
+          pb[nt][1] = transpose8x8(pack_half2(s[tt][nt][2] * sv[tt][1][g], s[tt][nt][3] * sv[tt][1][g]));
+        }
+        if constexpr (G == 1) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(ones[nt], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, pb[nt][0], pb[nt][1]);
+        }
+        // lane (r, c): elements g GROUP + r GROUP / 8 + 0..GROUP / 8 - 1 of positions pi(2c), pi(2c + 1), + 8
+        uint32_t w[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint8_t* at = vt + tt * C::CODE_BYTES + (t >> 1) * (C::CODE_BYTES / 2) + v_at[g][t & 1];
+          if constexpr (GROUP == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(at);
+            w[t][0] = x.x;
+            w[t][1] = x.y;
+          } else if constexpr (GROUP == 64) {
+            w[t][0] = *reinterpret_cast<const uint32_t*>(at);
+          } else {
+            w[t][0] = *reinterpret_cast<const uint16_t*>(at);
+          }
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < TPG / 2; ++q4) {    // four nibbles, two tiles of the output at a time
+          const uint32_t sel = (q4 & 1) ? 0x7632u : 0x5410u;
+          uint32_t xa[4], xb[4];
+          unpack4(__byte_perm(w[0][q4 >> 1], w[1][q4 >> 1], sel), xa);
+          unpack4(__byte_perm(w[2][q4 >> 1], w[3][q4 >> 1], sel), xb);
+          if constexpr (G > 1) {
+            // the 8 leaves each code here (below, it would take sums for every scale)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 e8 = bits_h2((j & 1) ? 0x00800080u : 0x00080008u);
+              xa[j] = h2_bits(__hsub2(bits_h2(xa[j]), e8));
+              xb[j] = h2_bits(__hsub2(bits_h2(xb[j]), e8));
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float(&o0)[4] = o[g * TPG + 2 * q4][nt], (&o1)[4] = o[g * TPG + 2 * q4 + 1][nt];
+            mma16816(o0, xa[0], xa[1], xb[0], xb[1], pb[nt][0], pb[nt][1]);
+            mma16816(o1, xa[2], xa[3], xb[2], xb[3], pb[nt][0], pb[nt][1]);
+          }
         }
       }
+    // The 8 in (code + 8) leaves the sums every fourth step: before it outgrows them.
+    if (G == 1 && ((i & 3) == 3 || i == mine - 1)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int t = 0; t < MT; ++t) o[t][nt][k] -= ones[nt][k];
+          ones[nt][k] = 0.f;
+        }
     }
   }
   cp_async_wait<0>();
@@ -562,80 +801,103 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(const __grid
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int t = 0; t < TPG; ++t) {
-          dst[g * GROUP + 2 * t] = o[g * TPG + t][nt][e];
-          dst[g * GROUP + 2 * t + 1] = o[g * TPG + t][nt][2 + e];
+        for (int t = 0; t < TPG; t += 2) {      // even nibbles in units of 2^-24, odd ones 2^-20
+          const float(&x)[4] = o[g * TPG + t][nt], (&y)[4] = o[g * TPG + t + 1][nt];
+          *reinterpret_cast<float4*>(dst + g * GROUP + 2 * t) =
+              make_float4(x[e] * 16777216.f, x[2 + e] * 1048576.f, y[e] * 16777216.f, y[2 + e] * 1048576.f);
         }
       if (r == 0) jml[warp * C::ROWS + row] = make_float2(m[nt][e], l[nt][e]);
     }
   __syncthreads();
-  for (int x = threadIdx.x; x < C::ROWS * (D / 2); x += 32 * kWarps) {
-    const int row = x / (D / 2), d = (x % (D / 2)) * 2;
+#pragma unroll
+  for (int i = threadIdx.x; i < C::ROWS * (D / 4); i += 32 * kWarps) {
+    const int row = i / (D / 4), d = (i % (D / 4)) * 4;
     const int rho = rt * C::ROWS + row;
     if (rho >= rows) continue;
-    float top = -1.0e30f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, jml[w * C::ROWS + row].x);
-    float sum = 0.f, v0 = 0.f, v1 = 0.f;
+    float2 ml[kWarps];
+    float top = -1.0e30f, sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = jml[w * C::ROWS + row];
-      const float f = exp2_fast(ml.x - top);
-      const float2 y = *reinterpret_cast<const float2*>(jo + (w * C::ROWS + row) * C::JOIN_STRIDE + d);
-      sum = fmaf(ml.y, f, sum);
-      v0 = fmaf(y.x, f, v0);
-      v1 = fmaf(y.y, f, v1);
+      ml[w] = jml[w * C::ROWS + row];
+      top = fmaxf(top, ml[w].x);
     }
-    const int qi = rho / a.ratio;
-    const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads * a.ratio) + h * a.ratio + rho - qi * a.ratio;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2_fast(ml[w].x - top);
+      const float4 x = *reinterpret_cast<const float4*>(jo + (w * C::ROWS + row) * C::JOIN_STRIDE + d);
+      sum = fmaf(ml[w].y, f, sum);
+      y = make_float4(fmaf(x.x, f, y.x), fmaf(x.y, f, y.y), fmaf(x.z, f, y.z), fmaf(x.w, f, y.w));
+    }
     if (a.splits == 1) {
+      const int qi = rho / a.ratio;
+      const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads * a.ratio) + h * a.ratio + rho - qi * a.ratio;
       const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;      // a row that sees nothing: zeros
-      *reinterpret_cast<uint32_t*>(a.out + orow * D + d) = pack_bf16x2(v0 * inv, v1 * inv);
+      *reinterpret_cast<uint2*>(a.out + orow * D + d) = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
     } else {
-      const int64_t prow = split * a.out_rows + orow;
-      *reinterpret_cast<float2*>(a.part_o + prow * D + d) = make_float2(v0, v1);
-      if (d == 0) a.part_ml[prow] = make_float2(top, sum);
+      *reinterpret_cast<float4*>(a.part_o + (part + row) * D + d) = y;
+      if (d == 0) a.part_ml[part + row] = make_float2(top, sum);
     }
   }
 }
 
-// Joins the splits of a row, in order: one warp per row, D / 32 values per lane.
-template <int D>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const float* __restrict__ part_o,
-                                                       const float2* __restrict__ part_ml, int64_t out_rows,
-                                                       int splits, uint16_t* __restrict__ out) {
+// Adds the splits' parts, one CTA per unit: two warps a row, each its half of
+// the splits in order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(64 * ROWS) kv4_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int E = D / 32;
+  __shared__ float part[ROWS][D + 2];
   grid_dependency_sync();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= out_rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = warp % ROWS, half = warp / ROWS;
+  const int unit = blockIdx.x;
+  const int rt = unit % a.row_tiles, h = unit / a.row_tiles % a.kv_heads, b = unit / a.row_tiles / a.kv_heads;
+  const int rho = rt * ROWS + row, qi = rho / a.ratio;
+  const bool live = rho < a.q_len * a.ratio;
+  auto part_row = [&](int s) { return (static_cast<int64_t>(s) * a.units + unit) * ROWS + row; };
   float top = -1.0e30f;
-  for (int s = lane; s < splits; s += 32) top = fmaxf(top, part_ml[s * out_rows + row].x);
+  if (live)
+    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[part_row(s)].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   float sum = 0.f, v[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) v[i] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = part_ml[s * out_rows + row];
-    const float f = exp2_fast(ml.x - top);
-    const float* p = part_o + (s * out_rows + row) * D + lane * E;
-    sum = fmaf(ml.y, f, sum);
-    if constexpr (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(p);
-      v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]), v[2] = fmaf(y.z, f, v[2]), v[3] = fmaf(y.w, f, v[3]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(p);
-      v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]);
+  const int mid = a.splits >> 1;
+  if (live) {
+#pragma unroll 8
+    for (int s = half ? mid : 0; s < (half ? a.splits : mid); ++s) {
+      const int64_t r = part_row(s);
+      const float2 ml = a.part_ml[r];
+      const float f = exp2_fast(ml.x - top);
+      const float* p = a.part_o + r * D + lane * E;
+      float y[E];
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        y[0] = x.x, y[1] = x.y;
+      }
+      sum = fmaf(ml.y, f, sum);
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = ml.y > 0.f ? fmaf(y[i], f, v[i]) : v[i];   // an empty part was not written
     }
   }
+  if (half == 1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) part[row][lane * E + i] = v[i];
+    if (lane == 0) part[row][D] = sum;
+  }
+  __syncthreads();
+  if (half == 1 || !live) return;
+  sum += part[row][D];
   const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(out + row * D + lane * 4) =
-        make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out + row * D + lane * 2) = pack_bf16x2(v[0] * inv, v[1] * inv);
+  const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads * a.ratio) + h * a.ratio + rho - qi * a.ratio;
+#pragma unroll
+  for (int i = 0; i < E; i += 2)
+    *reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E + i) =
+        pack_bf16x2((v[i] + part[row][lane * E + i]) * inv, (v[i + 1] + part[row][lane * E + i + 1]) * inv);
 }
 
 }  // namespace kv4

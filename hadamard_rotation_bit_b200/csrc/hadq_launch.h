@@ -119,18 +119,17 @@ ImmSplitVariant imm_split_for(int64_t m, bool out_bf16);
 ImmPairVariant imm_pair_for(bool out_bf16);
 int imm_fault_bits(int clear);
 
-// int4 cache: append, attention (rows = query rows per K/V head; the variant
-// takes `rows` of them per CTA) and the join of its splits.
+// int4 cache: append, and attention for `rows` query rows per K/V head: the
+// kernel (variant.rows of them per CTA, variant.ctas CTAs at once on an SM) and
+// the join of its splits.
 using AppendFn = void (*)(const kv4::AppendArgs);
 using AttnFn = void (*)(const kv4::AttnArgs);
-using JoinFn = void (*)(const float*, const float2*, int64_t, int, uint16_t*);
 struct AttnVariant {
-  AttnFn fn;
-  int threads, smem, rows;
+  AttnFn fn, join;
+  int threads, smem, rows, ctas;
 };
 AppendFn kv4_append_for(bool bf16, int d);
 AttnVariant kv4_attention_for(int d, int group, int rows);
-JoinFn kv4_join_for(int d);
 int kv4_fault_bits(int clear);
 
 // The tensor-core kernels' sticky fault words (bounded waits that ran out),

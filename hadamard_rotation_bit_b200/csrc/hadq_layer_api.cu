@@ -134,17 +134,6 @@ hadq_status check_block(int64_t block, int64_t head_dim, int* rotate) {
   return HADQ_OK;
 }
 
-// Splits of a sequence over CTAs.  Rule (sizes only, so that a captured call
-// and its workspace hold for any lengths): enough CTAs to fill 148 SMs with 4
-// each, and at least 8 tiles of 16 positions for a CTA's 4 warps.
-int kv4_splits(int64_t units, int64_t capacity) {
-  const int64_t want = ceil_div(148 * 4, std::max<int64_t>(units, 1));
-  const int64_t most = std::max<int64_t>(1, capacity / 128);
-  return static_cast<int>(std::min<int64_t>(std::min(want, most), 256));
-}
-
-int64_t kv4_row_tiles(int64_t rows) { return rows <= 8 ? 1 : ceil_div(rows, 16); }
-
 hadq_status check_attention_shape(int64_t batch, int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                   int64_t max_positions) {
   if (batch < 0) return invalid("batch must be >= 0");
@@ -155,14 +144,27 @@ hadq_status check_attention_shape(int64_t batch, int64_t q_len, int64_t heads, i
   if (heads > 65536 || batch > kMaxDim) return unsupported("batch or heads too large");
   if (max_positions < 1) return invalid("max_pages must be > 0");
   if (max_positions > kMaxDim) return unsupported("sequences of more than 2^30 positions");
-  if (batch * kv_heads * kv4_row_tiles(q_len * (heads / kv_heads)) > INT32_MAX) return unsupported("batch * heads too large");
+  if (batch * q_len * heads > INT32_MAX) return unsupported("batch * q_len * heads too large");
   return HADQ_OK;
 }
 
-int64_t attention_workspace(int64_t batch, int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                            int64_t max_positions, int* splits) {
-  *splits = kv4_splits(batch * kv_heads * kv4_row_tiles(q_len * (heads / kv_heads)), max_positions);
-  return *splits == 1 ? 0 : *splits * batch * q_len * heads * (head_dim + 2) * 4;
+// Splits of a sequence over CTAs, from sizes alone, so that a captured call and
+// its workspace hold for any lengths: about 1.75 CTAs for each that fits the GPU
+// at once (512 units: 60.7 us with 2 splits, 64.3 with 1, 64.4 with 3), but at
+// least 32 steps of 32 positions for a CTA (8 units of 32768 positions: 19.4 us
+// with 32 splits, 20.6 with 18, 23.8 with 64).
+int attention_splits(const hl::AttnVariant& v, int64_t units, int64_t max_positions) {
+  const int64_t slots = 148 * v.ctas, steps = ceil_div(max_positions, 32);
+  const int64_t want = (7 * slots + 2 * units) / (4 * units);
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, steps / 32)));
+}
+
+int64_t attention_units(const hl::AttnVariant& v, int64_t batch, int64_t rows, int64_t kv_heads) {
+  return batch * kv_heads * ceil_div(rows, v.rows);
+}
+
+int64_t attention_workspace(const hl::AttnVariant& v, int64_t units, int splits, int64_t head_dim) {
+  return splits == 1 ? 0 : splits * units * v.rows * (head_dim + 2) * 4;
 }
 
 }  // namespace
@@ -287,9 +289,13 @@ int64_t hadq_kv4_attention_workspace(int64_t batch, int64_t q_len, int64_t heads
   int64_t bytes = -1;
   const hadq_status st = entry([&]() -> hadq_status {
     const hadq_status s = check_attention_shape(batch, q_len, heads, kv_heads, head_dim, max_positions);
-    int splits = 0;
-    if (s == HADQ_OK) bytes = attention_workspace(batch, q_len, heads, kv_heads, head_dim, max_positions, &splits);
-    return s;
+    if (s != HADQ_OK) return s;
+    const int64_t rows = q_len * (heads / kv_heads);
+    // every group's variant has the same shape
+    const hl::AttnVariant v = hl::kv4_attention_for(static_cast<int>(head_dim), 32, static_cast<int>(rows));
+    const int64_t units = attention_units(v, batch, rows, kv_heads);
+    bytes = batch == 0 ? 0 : attention_workspace(v, units, attention_splits(v, units, max_positions), head_dim);
+    return HADQ_OK;
   });
   return st == HADQ_OK ? bytes : -1;
 }
@@ -323,8 +329,13 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
     Span cache[4];
     st = check_cache_pointers(c, cache);
     if (st != HADQ_OK) return st;
-    int splits = 0;
-    const int64_t need = attention_workspace(batch, q_len, heads, kv_heads, head_dim, max_pages * page_size, &splits);
+    const int ratio = static_cast<int>(heads / kv_heads);
+    const int64_t rows = q_len * ratio;
+    const hl::AttnVariant v = hl::kv4_attention_for(static_cast<int>(head_dim), static_cast<int>(group), static_cast<int>(rows));
+    if (v.fn == nullptr) return unsupported("no attention kernel for this head_dim and group");
+    const int64_t units = attention_units(v, batch, rows, kv_heads);
+    const int splits = attention_splits(v, units, max_pages * page_size);
+    const int64_t need = attention_workspace(v, units, splits, head_dim);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
       return invalid("workspace is smaller than hadq_kv4_attention_workspace says");
     const int64_t out_rows = batch * q_len * heads;
@@ -333,10 +344,6 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
                          span(lengths, batch * 4), cache[0], cache[1], cache[2], cache[3]};
     st = disjoint(outs, need > 0 ? 2 : 1, ins, 7, "out and workspace must not overlap an input or each other");
     if (st != HADQ_OK) return st;
-    const int ratio = static_cast<int>(heads / kv_heads);
-    const int64_t rows = q_len * ratio, row_tiles = kv4_row_tiles(rows);
-    const hl::AttnVariant v = hl::kv4_attention_for(static_cast<int>(head_dim), static_cast<int>(group), static_cast<int>(rows));
-    if (v.fn == nullptr) return unsupported("no attention kernel for this head_dim and group");
     hadq::kv4::AttnArgs p;
     p.q = static_cast<const uint16_t*>(q);
     p.q_stride = q_stride;
@@ -348,15 +355,15 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
     p.lengths = lengths;
     p.out = static_cast<uint16_t*>(out);
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + (need > 0 ? splits * out_rows * head_dim : 0));
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + (need > 0 ? splits * units * v.rows * head_dim : 0));
     p.num_pages = num_pages;
-    p.out_rows = out_rows;
     p.max_pages = static_cast<int>(max_pages);
     p.page_size = static_cast<int>(page_size);
     p.q_len = static_cast<int>(q_len);
     p.kv_heads = static_cast<int>(kv_heads);
     p.ratio = ratio;
-    p.row_tiles = static_cast<int>(row_tiles);
+    p.row_tiles = static_cast<int>(ceil_div(rows, v.rows));
+    p.units = static_cast<int>(units);
     p.splits = splits;
     p.rotate = rotate;
     p.norm = static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
@@ -367,13 +374,10 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
     st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
     if (st != HADQ_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(batch * kv_heads * row_tiles), static_cast<unsigned>(splits)),
-                                   1, v.threads, v.smem, s, p),
+    st = launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(units), static_cast<unsigned>(splits)), 1, v.threads, v.smem, s, p),
                        "cache attention launch");
     if (st != HADQ_OK || splits == 1) return st;
-    return launch_result(launch_pdl(hl::kv4_join_for(static_cast<int>(head_dim)), ceil_div(out_rows, 4), 128, 0, s,
-                                    const_cast<const float*>(p.part_o), const_cast<const float2*>(p.part_ml), out_rows, splits, p.out),
-                         "cache attention join launch");
+    return launch_result(launch_pdl(v.join, units, 64 * v.rows, 0, s, p), "cache attention join launch");
   });
 }
 

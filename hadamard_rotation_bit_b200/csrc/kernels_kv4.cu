@@ -9,8 +9,9 @@ namespace {
 
 template <int D, int GROUP, int NT>
 AttnVariant attn() {
-  using C = kv4::Cfg<D, GROUP, NT, 4>;
-  return AttnVariant{&kv4::kv4_attention_kernel<D, GROUP, NT, 4>, 32 * kv4::kWarps, C::SMEM_BYTES, C::ROWS};
+  using C = kv4::Cfg<D, GROUP, NT, 3>;
+  return AttnVariant{&kv4::kv4_attention_kernel<D, GROUP, NT, 3>, &kv4::kv4_join_kernel<D, C::ROWS>, 32 * kv4::kWarps,
+                     C::SMEM_BYTES, C::ROWS, NT == 1 ? 4 : 2};
 }
 
 template <int D, int GROUP>
@@ -29,10 +30,8 @@ AttnVariant kv4_attention_for(int d, int group, int rows) {
     if (group == 64) return attn_rows<64, 64>(rows);
     if (group == 32) return attn_rows<64, 32>(rows);
   }
-  return AttnVariant{nullptr, 0, 0, 0};
+  return AttnVariant{nullptr, nullptr, 0, 0, 0, 0};
 }
-
-JoinFn kv4_join_for(int d) { return d == 128 ? &kv4::kv4_join_kernel<128> : &kv4::kv4_join_kernel<64>; }
 
 AppendFn kv4_append_for(bool bf16, int d) {
   if (d == 128) return bf16 ? &kv4::kv4_append_kernel<true, 128> : &kv4::kv4_append_kernel<false, 128>;

@@ -116,7 +116,8 @@ def test_workspace_sizes(lib):
     f = H.hadq_kv4_attention_workspace
     assert f(0, 1, 8, 4, 128, 64) == 0
     assert f(1024, 1, 8, 4, 128, 1 << 20) == 0                     # enough sequences: no split
-    assert f(1, 1, 8, 4, 128, 1 << 20) % (8 * 130 * 4) == 0 and f(1, 1, 8, 4, 128, 1 << 20) > 0
+    assert f(1, 1, 8, 4, 128, 1 << 20) % (4 * 8 * 130 * 4) == 0 and f(1, 1, 8, 4, 128, 1 << 20) > 0
+    assert f(1, 1, 8, 4, 128, 64) == 0                             # too short
     for bad in ((-1, 1, 8, 4, 128, 64), (1, 0, 8, 4, 128, 64), (1, 1, 6, 4, 128, 64), (1, 1, 8, 4, 80, 64),
                 (1, 1, 8, 4, 128, 0), (1, 65, 8, 4, 128, 64)):
         assert lib.hadq_kv4_attention_workspace(*bad) == -1
