@@ -91,6 +91,10 @@ __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int* r) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -131,10 +135,11 @@ struct SplitCfg {
   static constexpr int TMEM_COLS = TN < 32 ? 32 : TN;
   static constexpr int THREADS = 128;
   static constexpr int SM_RING = 0;
-  static constexpr int SM_JOIN = STAGES * STAGE_BYTES;                // [source rank][column / 4 of mine][channel][4]
+  static constexpr int SM_JOIN = STAGES * STAGE_BYTES;                // [source rank][quad of columns][channel][4]
   static constexpr int SM_BARS = SM_JOIN + TN * 128 * 4;
   static constexpr int SM_SLOT = SM_BARS + 8 * (2 * STAGES + 1);
-  static constexpr int SMEM_BYTES = SM_SLOT + 16 + 1024;
+  static constexpr int SM_SA = SM_SLOT + 16;                          // the tokens' scales
+  static constexpr int SMEM_BYTES = SM_SA + TN * 4 + 1024;
 };
 
 // CTA (tile, rank): channels ch0 .. ch0 + 127, tokens t0 .. t0 + TN - 1, the
@@ -175,8 +180,23 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  if (splits > 1) cluster_arrive();           // matched before the first access to another CTA's memory
+  // While the previous kernel drains, ask L2 for the first weights (a hint: it
+  // reads nothing, so it may precede the wait).
+  if (threadIdx.x == 0)
+    for (int i = 0; i < min(iters, 3); ++i) prefetch_tile(&map_w, (s0 + i) * kSlice, ch0);
   grid_dependency_sync();
+  // What the epilogue reads, while the products run: a channel's scale and bias
+  // in its thread, the tokens' scales in shared memory.
+  float* sa = reinterpret_cast<float*>(smem + C::SM_SA);
+  const int ch = ch0 + threadIdx.x;           // TMEM lane = thread
+  const bool live = ch < p.n, biased = p.bias != nullptr;
+  float sw = 0.f, bias = 0.f;
+  if (warp >= 2 || lane != 0) {
+    if (warp >= 2)
+      for (int t = threadIdx.x - 64; t < TN; t += 64) sa[t] = t0 + t < p.m ? p.sa[t0 + t] : 0.f;
+    if (live) sw = p.sw[ch];
+    if (live && biased) bias = p.bias[ch];
+  }
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------- producer
@@ -215,18 +235,18 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   __syncwarp();
 
   // --------------------------------------------------------------- epilogue
+  if (warp < 2 && lane == 0) {                // the threads that fed the loop
+    if (live) sw = p.sw[ch];
+    if (live && biased) bias = p.bias[ch];
+  }
   bool ok = mbar_wait(done, 0);
   if (!ok && lane == 0) atomicOr(&tc::hadq_tc_fault, tc::kFaultEpilogue);
   ok = __all_sync(0xffffffffu, ok);
+  __syncthreads();                            // sa
   tc_fence_after();
-  const int ch = ch0 + threadIdx.x;           // TMEM lane = thread
-  const bool live = ch < p.n;
-  const float sw = live ? p.sw[ch] : 0.f;
-  const float bias = live && p.bias != nullptr ? p.bias[ch] : 0.f;
-  auto put = [&](int token, int acc) {
-    if (!live || token >= p.m) return;
-    store_one<OUT_BF16>(p.out, static_cast<int64_t>(token) * p.n + ch,
-                        finish(scaled(acc, p.sa[token]), sw, p.bias != nullptr, bias));
+  auto put = [&](int col, int acc) {          // column of the tile, its sum
+    if (live && t0 + col < p.m)
+      store_one<OUT_BF16>(p.out, static_cast<int64_t>(t0 + col) * p.n + ch, finish(scaled(acc, sa[col]), sw, biased, bias));
   };
   const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   if (splits == 1) {
@@ -237,35 +257,70 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         tmem_ld16i(taddr + c, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) put(t0 + c + j, v[j]);
+        for (int j = 0; j < 16; ++j) put(c + j, v[j]);
       }
     }
   } else {
     // Token column c goes to rank c / mine; there, the sources' sums are added
-    // (integers: in any order the same).
-    const int mine = TN / splits;             // 2 or more, a power of 2
+    // (integers: in any order the same).  Four columns of a channel travel
+    // together, or two where a rank has two.
+    const int mine = TN / splits, lg = __ffs(mine) - 1;   // 2 or more, a power of 2
     cluster_wait();
-    const uint32_t join = smem_u32(smem + C::SM_JOIN) + (rank * mine * 128 + threadIdx.x) * 4;
+    const uint32_t join = smem_u32(smem + C::SM_JOIN);
 #pragma unroll 1
     for (int c = 0; c < TN; c += 16) {
       int v[16];
-      if (ok) {
-        tmem_ld16i(taddr + c, v);
-        tmem_wait_ld();
-      }
+      tmem_ld16i(taddr + c, v);
+      tmem_wait_ld();
+      if (!ok) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int to = (c + j) / mine, col = (c + j) % mine;
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(join + col * 512, to)), "r"(ok ? v[j] : 0) : "memory");
+        for (int j = 0; j < 16; ++j) v[j] = 0;
+      }
+      if (mine >= 4) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const uint32_t at = join + (((rank << lg) + ((c + j) & (mine - 1))) * 128 + threadIdx.x * 4) * 4;
+          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_rank(at, (c + j) >> lg)), "r"(v[j]),
+                       "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3])
+                       : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const uint32_t at = join + (rank * 256 + threadIdx.x * 2) * 4;
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(map_rank(at, (c + j) >> 1)), "r"(v[j]), "r"(v[j + 1])
+                       : "memory");
+        }
       }
     }
     cluster_arrive();
     cluster_wait();
-    const int* got = reinterpret_cast<const int*>(smem + C::SM_JOIN) + threadIdx.x;
-    for (int col = 0; col < mine; ++col) {
-      int sum = 0;
-      for (int r = 0; r < splits; ++r) sum += got[(r * mine + col) * 128];
-      put(t0 + rank * mine + col, sum);
+    const int* got = reinterpret_cast<const int*>(smem + C::SM_JOIN);
+    if (mine >= 4) {
+#pragma unroll 2
+      for (int col = 0; col < mine; col += 4) {
+        int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < splits) {
+            const int4 x = *reinterpret_cast<const int4*>(got + ((r << lg) + col) * 128 + threadIdx.x * 4);
+            sum = make_int4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+          }
+        put(rank * mine + col, sum.x);
+        put(rank * mine + col + 1, sum.y);
+        put(rank * mine + col + 2, sum.z);
+        put(rank * mine + col + 3, sum.w);
+      }
+    } else {
+      int2 sum = make_int2(0, 0);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < splits) {
+          const int2 x = *reinterpret_cast<const int2*>(got + r * 256 + threadIdx.x * 2);
+          sum = make_int2(sum.x + x.x, sum.y + x.y);
+        }
+      put(rank * 2, sum.x);
+      put(rank * 2 + 1, sum.y);
     }
   }
   tc_fence_before();

@@ -18,7 +18,7 @@ ImmSplitVariant split(bool out_bf16) {
 ImmSplitVariant imm_split_for(int64_t m, bool out_bf16) {
   if (m <= 16) return split<16, 5>(out_bf16);
   if (m <= 32) return split<32, 4>(out_bf16);
-  if (m <= 64) return split<64, 3>(out_bf16);
+  if (m <= 64) return split<64, 6>(out_bf16);
   return split<128, 4>(out_bf16);
 }
 

@@ -459,32 +459,32 @@ def _invalid(message: str) -> HadqError:
     return HadqError(HADQ_ERR_INVALID_ARG, message)
 
 
-def _takes(name: str, t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape, contiguous: bool = True) -> int:
-    """Address of a tensor that must have this device, dtype and shape (None: any extent)."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and dev.type == "cuda":
+def _takes(name: str, t: torch.Tensor, index: int, dtype: torch.dtype, shape, contiguous: bool = True) -> int:
+    """Address of a tensor that must lie on CUDA device ``index`` (-1: none, refused) and have this dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0:
         if not contiguous or t.is_contiguous():
             return t.data_ptr()
-    _on_device(name, t, dev)
+    if not t.is_cuda:
+        raise _invalid(f"{name} must be a CUDA tensor (got {t.device})")
+    if t.get_device() != index:
+        raise _invalid(f"{name} is on {t.device}, the first tensor is not")
     if t.dtype != dtype:
         raise _invalid(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != len(shape) or any(s is not None and s != g for s, g in zip(shape, t.shape)):
+    if t.shape != tuple(shape):
         raise _invalid(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if contiguous and not t.is_contiguous():
-        raise _invalid(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise _invalid(f"{name} must be contiguous")
 
 
-def _call(fn, dev: torch.device, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device current: on the stream given,
-    or on that device's current stream.  Outputs come from that device's
+def _call(fn, index: int, stream, *args) -> None:
+    """fn(*args, stream) with device ``index`` current: on the stream given, or
+    on that device's current stream.  Outputs come from that device's
     allocator, so a stream given explicitly is the caller's to order with their
     use, as elsewhere."""
-    index = dev.index
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream)
     if index == torch._C._cuda_getDevice():
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = fn(*args, handle)
     if status != HADQ_OK:
         _check(status)
@@ -498,7 +498,8 @@ def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     x + residual, or None without a residual.  residual_out may be x or residual."""
     lib = _lib or load_library()
     rows, n = _rows_n(x)
-    dev, dtype, shape = x.device, x.dtype, x.shape
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    lead = shape[:-1]
     xp = _takes("x", x, dev, dtype, shape)
     wp = _takes("weight", weight, dev, dtype, (n,))
     rp = op = None
@@ -512,9 +513,9 @@ def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.int8)
     if scales is None:
-        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        scales = x.new_empty(lead, dtype=torch.float32)
     cp = _takes("codes", codes, dev, torch.int8, shape)
-    sp = _takes("scales", scales, dev, torch.float32, shape[:-1])
+    sp = _takes("scales", scales, dev, torch.float32, lead)
     _call(lib.hadq_rmsnorm_quant, dev, stream, xp, _dtype_code(dtype), rows, n, rp, wp, eps, op, cp, sp)
     return codes, scales, residual_out
 
@@ -526,7 +527,7 @@ def hadq_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
     and weights w [cols, k] (see include/hadq.h)."""
     lib = _lib or load_library()
     rows, k = _rows_n(a)
-    dev, lead = a.device, a.shape[:-1]
+    dev, lead = a.get_device(), a.shape[:-1]
     ap = _takes("a", a, dev, torch.int8, a.shape)
     asp = _takes("a_scales", a_scales, dev, torch.float32, lead)
     cols = w.shape[0] if w.dim() else 0
@@ -534,7 +535,7 @@ def hadq_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
     wsp = _takes("w_scales", w_scales, dev, torch.float32, (cols,))
     bp = None if bias is None else _takes("bias", bias, dev, torch.float32, (cols,))
     if out is None:
-        out = torch.empty((*lead, cols), dtype=out_dtype, device=dev)
+        out = a.new_empty((*lead, cols), dtype=out_dtype)
     op = _takes("out", out, dev, out.dtype, (*lead, cols))
     _call(lib.hadq_matmul_int8, dev, stream, ap, asp, rows, wp, wsp, cols, k, bp, op, _dtype_code(out.dtype))
     return out
@@ -583,7 +584,7 @@ def hadq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cod
     k, v: [tokens, kv_heads, head_dim], tokens at any even spacing; slots: int64,
     negative for tokens that are not stored."""
     lib = _lib or load_library()
-    dev, dtype = k.device, k.dtype
+    dev, dtype = k.get_device(), k.dtype
     ptrs, pages, heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
     tokens = k.shape[0] if k.dim() else 0
     kp = _takes("k", k, dev, dtype, (tokens, heads, d), contiguous=False)
@@ -611,7 +612,7 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
     (or [batch, heads, head_dim]) over the paged int4 cache (see include/hadq.h).
     scale: 1 / sqrt(head_dim) when None.  Without ``workspace`` one is allocated."""
     lib = _lib or load_library()
-    dev, dtype, shape = q.device, q.dtype, q.shape
+    dev, dtype, shape = q.get_device(), q.dtype, q.shape
     ptrs, pages, kv_heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
     if len(shape) not in (3, 4):
         raise _invalid("q must be [batch, q_len, heads, head_dim] or [batch, heads, head_dim]")
@@ -623,16 +624,15 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
     tp = _takes("page_table", page_table, dev, torch.int32, (batch, max_pages))
     lp = _takes("lengths", lengths, dev, torch.int32, (batch,))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     op = _takes("out", out, dev, dtype, shape)
     nbytes, ws = 0, None
     if workspace is None:
         need = lib.hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None:
-        _on_device("workspace", workspace, dev)
-        _holds("workspace", workspace, 0)
+        _takes("workspace", workspace, dev, workspace.dtype, workspace.shape)
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call(lib.hadq_kv4_attention, dev, stream, qp, qs, _dtype_code(dtype), batch, q_len, heads, kv_heads, d, block, group,
           *ptrs, pages, size, tp, max_pages, lp, d ** -0.5 if scale is None else scale, op, ws, nbytes)
