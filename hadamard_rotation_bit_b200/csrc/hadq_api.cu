@@ -986,7 +986,8 @@ hadq_impl hadq_get_impl(void) { return static_cast<hadq_impl>(g_impl.load(std::m
 int hadq_device_faults(int clear) {
   const int a = hadq::launch::tc_fault_bits(clear), b = hadq::launch::tck_fault_bits(clear);
   const int c = hadq::launch::kv4_fault_bits(clear), d = hadq::launch::imm_fault_bits(clear);
-  return a < 0 || b < 0 || c < 0 || d < 0 ? -1 : (a | b | c | d);
+  const int e = hadq::launch::norm_fault_bits(clear);
+  return a < 0 || b < 0 || c < 0 || d < 0 || e < 0 ? -1 : (a | b | c | d | e);
 }
 
 }  // extern "C"

@@ -95,13 +95,21 @@ KsFn staged_kernel_bf16(int k, int shi, int mode, int sgk);
 // (block = row), or OUT_INT4 / OUT_MXFP4 / OUT_NVFP4.
 TckVariant tck_kernel_for(int k, int hi, int mode);
 
-// Norm kernels: rows per CTA and threads of the variant for a row length.
+// Norm kernels: rows per CTA and threads of the variant for a row length, and
+// the kernel for many rows (its ring in dynamic shared memory).
 using NormFn = void (*)(const void*, const void*, const void*, int64_t, int, float, void*, int8_t*, float*);
 struct NormVariant {
   NormFn fn;
   int threads, rows_per_cta;
 };
 NormVariant norm_kernel_for(bool bf16, bool residual, int64_t rows, int64_t n);
+using NormRingFn = void (*)(const void*, const void*, const void*, int64_t, int, float, void*, int8_t*, float*, int);
+struct NormRingVariant {
+  NormRingFn fn;
+  int threads;
+};
+NormRingVariant norm_ring_for(bool bf16, bool residual, int64_t n);
+int norm_fault_bits(int clear);
 
 // int8 matrix product: the kernel for few tokens (up to `tokens` per CTA) and
 // the one for many.

@@ -507,15 +507,21 @@ def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         rp = _takes("residual", residual, dev, dtype, shape)
         if residual_out is None:
             residual_out = torch.empty_like(x)
-        op = _takes("residual_out", residual_out, dev, dtype, shape)
+            op = residual_out.data_ptr()
+        else:
+            op = _takes("residual_out", residual_out, dev, dtype, shape)
     elif residual_out is not None:
         raise _invalid("residual_out needs a residual")
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.int8)
+        cp = codes.data_ptr()
+    else:
+        cp = _takes("codes", codes, dev, torch.int8, shape)
     if scales is None:
         scales = x.new_empty(lead, dtype=torch.float32)
-    cp = _takes("codes", codes, dev, torch.int8, shape)
-    sp = _takes("scales", scales, dev, torch.float32, lead)
+        sp = scales.data_ptr()
+    else:
+        sp = _takes("scales", scales, dev, torch.float32, lead)
     _call(lib.hadq_rmsnorm_quant, dev, stream, xp, _dtype_code(dtype), rows, n, rp, wp, eps, op, cp, sp)
     return codes, scales, residual_out
 
@@ -536,8 +542,11 @@ def hadq_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
     bp = None if bias is None else _takes("bias", bias, dev, torch.float32, (cols,))
     if out is None:
         out = a.new_empty((*lead, cols), dtype=out_dtype)
-    op = _takes("out", out, dev, out.dtype, (*lead, cols))
-    _call(lib.hadq_matmul_int8, dev, stream, ap, asp, rows, wp, wsp, cols, k, bp, op, _dtype_code(out.dtype))
+        op = out.data_ptr()
+    else:
+        out_dtype = out.dtype
+        op = _takes("out", out, dev, out_dtype, (*lead, cols))
+    _call(lib.hadq_matmul_int8, dev, stream, ap, asp, rows, wp, wsp, cols, k, bp, op, _dtype_code(out_dtype))
     return out
 
 
@@ -625,7 +634,9 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
     lp = _takes("lengths", lengths, dev, torch.int32, (batch,))
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    op = _takes("out", out, dev, dtype, shape)
+        op = out.data_ptr()
+    else:
+        op = _takes("out", out, dev, dtype, shape)
     nbytes, ws = 0, None
     if workspace is None:
         need = lib.hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)

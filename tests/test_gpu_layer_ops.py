@@ -59,7 +59,8 @@ def check_norm(x, w, eps, residual, codes, scales, stream):
 @pytest.mark.parametrize("res", [False, True])
 @pytest.mark.parametrize("rows,n", [(1, 8), (3, 16), (130, 72), (5, 248), (7, 256), (9, 264), (33, 512), (3, 520),
                                     (777, 1000), (2, 1024), (3, 1032), (5, 2048), (3, 2056), (300, 4096), (1, 4096),
-                                    (3, 4104), (2, 8192), (3, 8200), (2, 14336), (2, 16384), (3, 16392), (2, 32768)])
+                                    (3, 4104), (4099, 2064), (5000, 4096), (1001, 4104), (1500, 8192), (1000, 14336),
+                                    (1203, 16384), (2, 8192), (3, 8200), (2, 14336), (2, 16384), (3, 16392), (2, 32768)])
 def test_norm(rows, n, dtype, res):
     g, dt = gen(rows + n), DTYPES[dtype]
     x = randn(g, rows, n, dtype=dt)
