@@ -148,6 +148,12 @@ hadq_status check_cache_pointers(const Cache& c, Span (&spans)[4]) {
   return disjoint(spans, 4, nullptr, 0, "the cache's four tensors must not overlap");
 }
 
+hadq::kv4::Divider divider(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return hadq::kv4::Divider{static_cast<uint32_t>((uint64_t(1) << (31 + s)) / d + 1), s, d};
+}
+
 // block: the whole head, or 1 (H_1: none).
 hadq_status check_block(int64_t block, int64_t head_dim, int* rotate) {
   if (block == 0 || block == -1 || block == head_dim) *rotate = 1;
@@ -288,6 +294,7 @@ hadq_status hadq_kv4_append(const void* k, int64_t k_stride, const void* v, int6
     if (k_stride < width || v_stride < width) return invalid("k_stride and v_stride must be at least kv_heads * head_dim");
     if (k_stride % unit != 0 || v_stride % unit != 0) return fail(HADQ_ERR_MISALIGNED, "k_stride and v_stride must be multiples of 16 bytes");
     if (tokens > kMaxDim || k_stride > kMaxDim || v_stride > kMaxDim) return unsupported("tokens and strides must be at most 2^30");
+    if (tokens * kv_heads > INT32_MAX) return unsupported("tokens * kv_heads must be below 2^31");
     if (tokens == 0) return HADQ_OK;
     if (!k || !v || !slots) return invalid("null pointer");
     if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return fail(HADQ_ERR_MISALIGNED, "k, v and slots must be 16-byte aligned");
@@ -305,18 +312,16 @@ hadq_status hadq_kv4_append(const void* k, int64_t k_stride, const void* v, int6
     p.codes[0] = static_cast<uint8_t*>(k_codes), p.codes[1] = static_cast<uint8_t*>(v_codes);
     p.scales[0] = static_cast<__half*>(k_scales), p.scales[1] = static_cast<__half*>(v_scales);
     p.slots = slots;
-    p.tokens = tokens;
+    p.rows = static_cast<uint32_t>(tokens * kv_heads);
     p.num_slots = num_pages * page_size;
-    p.kv_heads = static_cast<int>(kv_heads);
-    p.page_size = static_cast<int>(page_size);
+    p.kv_heads = divider(static_cast<uint32_t>(kv_heads));
+    p.page_size = divider(static_cast<uint32_t>(page_size));
     p.group = static_cast<int>(group);
     p.rotate_k = rotate;
     p.norm = static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
-    const int64_t grid = ceil_div(tokens * kv_heads * (head_dim / 32), 256);
-    if (grid > INT32_MAX) return unsupported("too many rows");
-    return launch_result(launch_pdl3(hl::kv4_append_for(dtype == HADQ_BF16, static_cast<int>(head_dim)),
-                                     dim3(static_cast<unsigned>(grid), 2), 1, 256, 0, static_cast<cudaStream_t>(stream), p),
-                         "cache append launch");
+    const hl::AppendFn fn = hl::kv4_append_for(dtype == HADQ_BF16, static_cast<int>(head_dim));
+    const int64_t grid = 2 * ceil_div(tokens * kv_heads * (head_dim / 32), 256);
+    return launch_result(launch_pdl(fn, grid, 256, 0, static_cast<cudaStream_t>(stream), p), "cache append launch");
   });
 }
 
