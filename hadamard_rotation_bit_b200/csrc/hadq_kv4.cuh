@@ -235,6 +235,22 @@ __device__ __forceinline__ void mma16832(int (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with sums that start at 0.
+template <bool SIGNED>
+__device__ __forceinline__ void mma16832_from0(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  if constexpr (SIGNED)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -291,6 +307,31 @@ __device__ __forceinline__ int v_chunk(int t, int ch) {
   else return t * 32 + (ch << 4);
 }
 
+constexpr uint32_t kNoTile = 0xFFFFFFFFu;     // a page outside the cache
+
+// A step's copies where a sequence ends or a page lies outside the cache: zeros
+// in place of what must not be read (the positions are masked).  Out of line:
+// the loop's code stays short.
+template <int D, int G>
+__device__ __noinline__ void copy_partial(uint32_t dst, const uint8_t* k_lane, const uint8_t* v_lane, const uint8_t* s_lane,
+                                          uint32_t e0, uint32_t e1, int n0, int n1) {
+  constexpr int NG = D / 32, CODE_BYTES = 8 * D, SCALE_BYTES = 32 * G;
+  const int lane = threadIdx.x & 31;
+  const uint64_t f0 = e0 == kNoTile ? 0 : e0, f1 = e1 == kNoTile ? 0 : e1;
+  for (int u = 0; u < D / 64; ++u) {
+    const int j = lane + 32 * u, t = j / NG, b0 = t < n0 ? 16 : 0, b1 = t < n1 ? 16 : 0;
+    const uint32_t k = dst + k_chunk<D, G>(t, j % NG), v = dst + 2 * CODE_BYTES + v_chunk<D>(t, j % NG);
+    cp_async16(k, k_lane + f0 * CODE_BYTES + 512 * u, b0);
+    cp_async16(k + CODE_BYTES, k_lane + f1 * CODE_BYTES + 512 * u, b1);
+    cp_async16(v, v_lane + f0 * CODE_BYTES + 512 * u, b0);
+    cp_async16(v + CODE_BYTES, v_lane + f1 * CODE_BYTES + 512 * u, b1);
+  }
+  const int bytes = min(max((lane < 16 ? n0 : n1) * 2 * G - 16 * (lane & 7), 0), 16);
+  if ((lane & 7) < 2 * G)
+    cp_async16(dst + 4 * CODE_BYTES + ((lane >> 4) + ((lane & 8) ? 2 : 0)) * SCALE_BYTES + 16 * (lane & 7),
+               s_lane + (lane < 16 ? f0 : f1) * SCALE_BYTES, bytes);
+}
+
 __device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
   const int n = a.lengths[b], most = a.max_pages * a.page_size;
   return n < 0 ? 0 : n > most ? most : n;
@@ -318,6 +359,20 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   const int rows = a.q_len * a.ratio;
   const int unit = blockIdx.x, split = blockIdx.y;
   const int rt = unit % a.row_tiles, h = unit / a.row_tiles % a.kv_heads, b = unit / a.row_tiles / a.kv_heads;
+  // the query's values, on their way while the length and the page table are read
+  constexpr int LPR = D / 8, PASS = kWarps * 32 / LPR;        // lanes per row, rows of a pass of all warps
+  constexpr int PASSES = (C::ROWS + PASS - 1) / PASS;
+  uint4 qraw[PASSES];
+#pragma unroll
+  for (int ps = 0; ps < PASSES; ++ps) {
+    const int row = ps * PASS + threadIdx.x / LPR, rho = rt * C::ROWS + row;
+    qraw[ps] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < C::ROWS && rho < rows) {
+      const int i = rho / a.ratio, head = h * a.ratio + rho - i * a.ratio;
+      qraw[ps] = ldg_stream(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride +
+                                                           static_cast<int64_t>(head) * D + 8 * (threadIdx.x % LPR)));
+    }
+  }
   const int len = length_of(a, b);
   if (threadIdx.x == 0 && len != a.lengths[b]) atomicOr(&hadq_kv4_fault, kFaultLength);
   const int64_t part = (static_cast<int64_t>(split) * a.units + unit) * C::ROWS;   // first row in the workspace
@@ -332,7 +387,6 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   // ---- copies.  Lane l holds the entry of tile l & 1 of the warp's step
   // i0 + l / 2: the number of the 16-position run in the cache (fewer than
   // 2^32: a run takes 512 bytes or more), or kNoTile for a page outside it.
-  constexpr uint32_t kNoTile = 0xFFFFFFFFu;
   uint32_t entry = kNoTile;
   const int blocks = a.page_size >> 4;
   auto load_entries = [&](int i0) {
@@ -378,46 +432,28 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
         }
         if (s_live) cp_async16(st + s_dst, s_lane + static_cast<uint64_t>(es) * TILE_SCALES);
       } else {
-        // the end of a sequence, or a page outside the cache: zeros in place
-        // of what must not be read, and masked below
         const int n0 = e0 == kNoTile ? 0 : min(16, left), n1 = e1 == kNoTile ? 0 : min(16, max(left - 16, 0));
         if (lane == 0) nvalid[i % STAGES] = make_int2(n0, n1);
-        const uint64_t f0 = e0 == kNoTile ? 0 : e0, f1 = e1 == kNoTile ? 0 : e1;
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u) {
-          const int t = (lane + 32 * u) / NG, b0 = t < n0 ? 16 : 0, b1 = t < n1 ? 16 : 0;
-          cp_async16(st + k_dst[u], k_lane + f0 * C::CODE_BYTES + 512 * u, b0);
-          cp_async16(st + k_dst[u] + C::CODE_BYTES, k_lane + f1 * C::CODE_BYTES + 512 * u, b1);
-          cp_async16(st + v_dst[u], v_lane + f0 * C::CODE_BYTES + 512 * u, b0);
-          cp_async16(st + v_dst[u] + C::CODE_BYTES, v_lane + f1 * C::CODE_BYTES + 512 * u, b1);
-        }
-        const int bytes = min(max((lane < 16 ? n0 : n1) * 2 * G - 16 * (lane & 7), 0), 16);
-        if (s_live) cp_async16(st + s_dst, s_lane + (lane < 16 ? f0 : f1) * TILE_SCALES, bytes);
+        copy_partial<D, G>(ring_u + st, k_lane, v_lane, s_lane, e0, e1, n0, n1);
       }
     }
     cp_async_commit();
   };
-#pragma unroll
+#pragma unroll 1                              // the code is fetched once
   for (int i = 0; i < STAGES - 1; ++i) issue(i);
 
   // ---- query rows.  A lane's words of a K row, w = 0 .. NG - 1: with one scale
   // per row elements c D / 4 + 8 w .. (consecutive: one load), else 32 w + 8 c ..
   // (every word in a group of its own).  D / 8 lanes rotate a row, 8 elements
   // each, and leave it in the order in which lane (r, c) takes row r.
-  constexpr int LPR = D / 8, PASS = kWarps * 32 / LPR;        // rows of a pass of all warps
-  constexpr int PASSES = (C::ROWS + PASS - 1) / PASS;
   uint4* qs = reinterpret_cast<uint4*>(smem + C::Q_AT);       // [row / 8][word][lane]
   float* tops = reinterpret_cast<float*>(smem + C::Q_AT + C::Q_BYTES);
   float v[PASSES][8], f = a.scale_log2;
   if (a.rotate) f *= a.norm;
 #pragma unroll
   for (int ps = 0; ps < PASSES; ++ps) {
-    const int row = ps * PASS + threadIdx.x / LPR, rho = rt * C::ROWS + row, part8 = threadIdx.x % LPR;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (row < C::ROWS && rho < rows) {
-      const int i = rho / a.ratio, head = h * a.ratio + rho - i * a.ratio;
-      w = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride + static_cast<int64_t>(head) * D + 8 * part8);
-    }
+    const int part8 = threadIdx.x % LPR;
+    const uint4 w = qraw[ps];
     unpack_bf16x2(w.x, v[ps][0], v[ps][1]);
     unpack_bf16x2(w.y, v[ps][2], v[ps][3]);
     unpack_bf16x2(w.z, v[ps][4], v[ps][5]);
@@ -474,23 +510,24 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   }
   __syncthreads();
   uint32_t qb[NT][NG][4];
-  float bias[NT][G][4];                       // G > 1: what the 8 in (code + 8) adds to a row's sums, negative
+  float bias[NT][G][2];                       // G > 1: what the 8 in (code + 8) adds to a row's sums, negative
   int limit[NT][2];                           // first position that rows 2c, 2c + 1 do not see
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) bias[nt][g][k] = 0.f;
+      float eight[4] = {0.f, 0.f, 0.f, 0.f};  // equal for every row of the product
 #pragma unroll
       for (int w = g * (GROUP / 32); w < (g + 1) * (GROUP / 32); ++w) {
         const uint4 x = qs[(nt * NG + w) * 32 + lane];
         qb[nt][w][0] = x.x, qb[nt][w][1] = x.y, qb[nt][w][2] = x.z, qb[nt][w][3] = x.w;
         if constexpr (G > 1) {
-          mma16816(bias[nt][g], 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.x, x.y);
-          mma16816(bias[nt][g], 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.z, x.w);
+          mma16816(eight, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.x, x.y);
+          mma16816(eight, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.z, x.w);
         }
       }
+      bias[nt][g][0] = eight[0];
+      bias[nt][g][1] = eight[1];
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -575,12 +612,6 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
       if constexpr (G == 1) {
         int high[2][NT][4], low[2][NT][4];
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) high[tt][nt][k] = low[tt][nt][k] = 0;
-#pragma unroll
         for (int w = 0; w < NG; ++w)
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt) {
@@ -589,8 +620,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
             const uint32_t a1 = (kw[tt][1][w] << 4) & 0xF0F0F0F0u, a3 = kw[tt][1][w] & 0xF0F0F0F0u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16832<true>(high[tt][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
-              mma16832<false>(low[tt][nt], a0, a1, a2, a3, qb[nt][w][2], qb[nt][w][3]);
+              if (w == 0) {
+                mma16832_from0<true>(high[tt][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
+                mma16832_from0<false>(low[tt][nt], a0, a1, a2, a3, qb[nt][w][2], qb[nt][w][3]);
+              } else {
+                mma16832<true>(high[tt][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
+                mma16832<false>(low[tt][nt], a0, a1, a2, a3, qb[nt][w][2], qb[nt][w][3]);
+              }
             }
           }
 #pragma unroll
@@ -605,7 +641,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[tt][nt][k] = bias[nt][g][k];
+            for (int k = 0; k < 4; ++k) acc[tt][nt][k] = bias[nt][g][k & 1];
 #pragma unroll
         for (int w = 0; w < GROUP / 32; ++w)
 #pragma unroll
