@@ -170,8 +170,10 @@ struct AttnArgs {
   float2* part_ml;           // [split][unit][rows of a tile]: maximum, sum
   int64_t num_pages;
   int max_pages, page_size;
-  int q_len, kv_heads, ratio;   // heads = kv_heads * ratio
-  int row_tiles;
+  int q_len;
+  Divider kv_heads, ratio;   // heads = kv_heads * ratio
+  Divider row_tiles;
+  Divider blocks;            // page_size / 16
   int units, splits;
   int rotate;
   float norm;                // fp32(1 / sqrt(D))
@@ -356,9 +358,10 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   int2* nvalid = reinterpret_cast<int2*>(smem + C::VALID_AT) + warp * STAGES;
 
   grid_dependency_sync();
-  const int rows = a.q_len * a.ratio;
+  const int ratio = a.ratio.d, rows = a.q_len * ratio;
   const int unit = blockIdx.x, split = blockIdx.y;
-  const int rt = unit % a.row_tiles, h = unit / a.row_tiles % a.kv_heads, b = unit / a.row_tiles / a.kv_heads;
+  const int bh = static_cast<int>(a.row_tiles(unit)), rt = unit - bh * a.row_tiles.d;
+  const int b = static_cast<int>(a.kv_heads(bh)), h = bh - b * a.kv_heads.d;
   // the query's values, on their way while the length and the page table are read
   constexpr int LPR = D / 8, PASS = kWarps * 32 / LPR;        // lanes per row, rows of a pass of all warps
   constexpr int PASSES = (C::ROWS + PASS - 1) / PASS;
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     const int row = ps * PASS + threadIdx.x / LPR, rho = rt * C::ROWS + row;
     qraw[ps] = make_uint4(0u, 0u, 0u, 0u);
     if (row < C::ROWS && rho < rows) {
-      const int i = rho / a.ratio, head = h * a.ratio + rho - i * a.ratio;
+      const int i = static_cast<int>(a.ratio(rho)), head = h * ratio + rho - i * ratio;
       qraw[ps] = ldg_stream(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride +
                                                            static_cast<int64_t>(head) * D + 8 * (threadIdx.x % LPR)));
     }
@@ -388,15 +391,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   // i0 + l / 2: the number of the 16-position run in the cache (fewer than
   // 2^32: a run takes 512 bytes or more), or kNoTile for a page outside it.
   uint32_t entry = kNoTile;
-  const int blocks = a.page_size >> 4;
   auto load_entries = [&](int i0) {
     const int tile = (t0 + warp + (i0 + (lane >> 1)) * kWarps) * 2 + (lane & 1);
     entry = kNoTile;
     if (tile * 16 < len) {
-      const int p = tile / blocks;
+      const int p = static_cast<int>(a.blocks(tile));
       const int page = a.table[static_cast<int64_t>(b) * a.max_pages + p];
       if (page < 0 || page >= a.num_pages) atomicOr(&hadq_kv4_fault, kFaultPage);
-      else entry = (static_cast<uint32_t>(page) * a.kv_heads + h) * blocks + (tile - p * blocks);
+      else entry = (static_cast<uint32_t>(page) * a.kv_heads.d + h) * a.blocks.d + (tile - p * a.blocks.d);
     }
   };
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
@@ -414,15 +416,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     k_dst[u] = ring_u + k_chunk<D, G>(j / NG, j % NG);
     v_dst[u] = ring_u + 2 * C::CODE_BYTES + v_chunk<D>(j / NG, j % NG);
   }
-  auto issue = [&](int i) {
+  auto issue = [&](int i, int stage) {
     if (i < mine) {
       if ((i & 15) == 0) load_entries(i);
       const uint32_t e0 = __shfl_sync(0xffffffffu, entry, (i & 15) * 2), e1 = __shfl_sync(0xffffffffu, entry, (i & 15) * 2 + 1);
-      const uint32_t st = (i % STAGES) * C::STAGE_BYTES;
+      const uint32_t st = stage * C::STAGE_BYTES;
       const int left = len - (t0 + warp + i * kWarps) * 32;
       const uint32_t es = lane < 16 ? e0 : e1;
       if (left >= 32 && e0 != kNoTile && e1 != kNoTile) {
-        if (lane == 0) nvalid[i % STAGES] = make_int2(16, 16);
+        if (lane == 0) nvalid[stage] = make_int2(16, 16);
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
           cp_async16(st + k_dst[u], k_lane + static_cast<uint64_t>(e0) * C::CODE_BYTES + 512 * u);
@@ -433,14 +435,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
         if (s_live) cp_async16(st + s_dst, s_lane + static_cast<uint64_t>(es) * TILE_SCALES);
       } else {
         const int n0 = e0 == kNoTile ? 0 : min(16, left), n1 = e1 == kNoTile ? 0 : min(16, max(left - 16, 0));
-        if (lane == 0) nvalid[i % STAGES] = make_int2(n0, n1);
+        if (lane == 0) nvalid[stage] = make_int2(n0, n1);
         copy_partial<D, G>(ring_u + st, k_lane, v_lane, s_lane, e0, e1, n0, n1);
       }
     }
     cp_async_commit();
   };
 #pragma unroll 1                              // the code is fetched once
-  for (int i = 0; i < STAGES - 1; ++i) issue(i);
+  for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
 
   // ---- query rows.  A lane's words of a K row, w = 0 .. NG - 1: with one scale
   // per row elements c D / 4 + 8 w .. (consecutive: one load), else 32 w + 8 c ..
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int col = rt * C::ROWS + nt * 8 + 2 * c + e;
-      limit[nt][e] = len - a.q_len + 1 + (col < rows ? col / a.ratio : 0);
+      limit[nt][e] = len - a.q_len + 1 + static_cast<int>(a.ratio(col));
     }
   }
 
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     for (int e = 0; e < 2; ++e) m[nt][e] = -1.0e30f, l[nt][e] = 0.f, ones[nt][e] = ones[nt][2 + e] = 0.f;
 
   // positions below this are seen by every row of the tile
-  const int seen_by_all = len - a.q_len + 1 + (rt * C::ROWS) / a.ratio;
+  const int seen_by_all = len - a.q_len + 1 + static_cast<int>(a.ratio(rt * C::ROWS));
 
   // Row i of a tile's products is position pi(i): pi(2c) = c, pi(2c + 1) = 4 +
   // (c ^ 1), pi(i + 8) = pi(i) + 8.  The four lanes c then read four
@@ -575,16 +577,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
       else v_at[g][e] = v_chunk<D>(t, g) + r * 2;
     }
 
+  int stage = 0;
 #pragma unroll 1
   for (int i = 0; i < mine; ++i) {
     cp_async_wait<STAGES - 2>();
     __syncwarp();
-    issue(i + STAGES - 1);                    // into the stage consumed in the last round
-    const uint8_t* kt = ring + (i % STAGES) * C::STAGE_BYTES;
+    issue(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);   // the stage consumed in the last round
+    const uint8_t* kt = ring + stage * C::STAGE_BYTES;
     const uint8_t* vt = kt + 2 * C::CODE_BYTES;
     const __half* kst = reinterpret_cast<const __half*>(kt + 4 * C::CODE_BYTES) + pr * G;
     const __half* vst = kst + 32 * G;
-    const int2 nv = nvalid[i % STAGES];
+    const int2 nv = nvalid[stage];
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
     const int pos = (t0 + warp + i * kWarps) * 32;
 
     // ---- S^T = K q^T: s times kk are the base-2 scores
@@ -877,8 +881,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
       y = make_float4(fmaf(x.x, f, y.x), fmaf(x.y, f, y.y), fmaf(x.z, f, y.z), fmaf(x.w, f, y.w));
     }
     if (a.splits == 1) {
-      const int qi = rho / a.ratio;
-      const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads * a.ratio) + h * a.ratio + rho - qi * a.ratio;
+      const int qi = static_cast<int>(a.ratio(rho));
+      const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads.d * ratio) + h * ratio + rho - qi * ratio;
       const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;      // a row that sees nothing: zeros
       *reinterpret_cast<uint2*>(a.out + orow * D + d) = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
     } else {
@@ -898,9 +902,10 @@ __global__ void __launch_bounds__(64 * ROWS) kv4_join_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = warp % ROWS, half = warp / ROWS;
   const int unit = blockIdx.x;
-  const int rt = unit % a.row_tiles, h = unit / a.row_tiles % a.kv_heads, b = unit / a.row_tiles / a.kv_heads;
-  const int rho = rt * ROWS + row, qi = rho / a.ratio;
-  const bool live = rho < a.q_len * a.ratio;
+  const int bh = static_cast<int>(a.row_tiles(unit)), rt = unit - bh * a.row_tiles.d;
+  const int b = static_cast<int>(a.kv_heads(bh)), h = bh - b * a.kv_heads.d;
+  const int ratio = a.ratio.d, rho = rt * ROWS + row, qi = static_cast<int>(a.ratio(rho));
+  const bool live = rho < a.q_len * ratio;
   auto part_row = [&](int s) { return (static_cast<int64_t>(s) * a.units + unit) * ROWS + row; };
   float top = -1.0e30f;
   if (live)
@@ -940,7 +945,7 @@ __global__ void __launch_bounds__(64 * ROWS) kv4_join_kernel(const __grid_consta
   if (half == 1 || !live) return;
   sum += part[row][D];
   const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
-  const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads * a.ratio) + h * a.ratio + rho - qi * a.ratio;
+  const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads.d * ratio) + h * ratio + rho - qi * ratio;
 #pragma unroll
   for (int i = 0; i < E; i += 2)
     *reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E + i) =

@@ -401,9 +401,10 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
     p.max_pages = static_cast<int>(max_pages);
     p.page_size = static_cast<int>(page_size);
     p.q_len = static_cast<int>(q_len);
-    p.kv_heads = static_cast<int>(kv_heads);
-    p.ratio = ratio;
-    p.row_tiles = static_cast<int>(ceil_div(rows, v.rows));
+    p.kv_heads = divider(static_cast<uint32_t>(kv_heads));
+    p.ratio = divider(static_cast<uint32_t>(ratio));
+    p.row_tiles = divider(static_cast<uint32_t>(ceil_div(rows, v.rows)));
+    p.blocks = divider(static_cast<uint32_t>(page_size / 16));
     p.units = static_cast<int>(units);
     p.splits = splits;
     p.rotate = rotate;
