@@ -6,10 +6,14 @@
 // memory).  The sums are exact for k < 131072, so their order is free: a split
 // of k adds up to the same bits, and every kernel here gives the same result.
 //
-// Two kernels.  Both stage 128-byte slices of k by TMA (128-byte swizzle; the
-// tail of k and rows beyond a matrix are filled with zeros) into a ring that
-// one thread feeds and one thread consumes.
+// Three kernels.
 //
+//   imm_row_kernel    a handful of tokens: bound by reading w, and by what it
+//       takes to begin.  Warps read rows of w straight from global memory and
+//       form four-way byte products; nothing is set up first.  4096 x 14336: 9.5
+//       us with 1 token (6.2 TB/s), 10.4 with 4, against 13.6 and 13.8 of the
+//       next kernel; with 8 tokens 17.3 against 13.8, the byte products'
+//       operands no longer fit beside the loads.
 //   imm_split_kernel  few tokens: bound by reading w.  Output channels are the
 //       MMA's 128 rows and TN tokens its columns, so one token costs no more
 //       traffic than it has, and the CTAs of a cluster share the k of a tile,
@@ -19,6 +23,10 @@
 //       and L2 reads per product of a single CTA's tile; persistent, two
 //       accumulators, so that the epilogue of a tile runs under the products
 //       of the next.
+//
+// The last two stage 128-byte slices of k by TMA (128-byte swizzle; the tail of
+// k and rows beyond a matrix are filled with zeros) into a ring that one thread
+// feeds and one thread consumes.
 #pragma once
 
 #include "hadq_tc.cuh"
@@ -123,6 +131,70 @@ template <bool OUT_BF16>
 __device__ __forceinline__ void store_one(void* out, int64_t e, float y) {
   if constexpr (OUT_BF16) static_cast<__nv_bfloat16*>(out)[e] = __float2bfloat16_rn(y);
   else static_cast<float*>(out)[e] = y;
+}
+
+// ---------------------------------------------------- a handful of tokens
+
+constexpr int kRowWarps = 8;
+
+// A warp takes four channels and one of `parts` runs of k (16-byte chunks, lane
+// by lane); the CTA's warps are 8 / parts such quads of channels.  M: tokens,
+// rounded up to 1, 2 or 4 (those beyond p.m repeat the last one, unwritten).
+template <int M, bool OUT_BF16>
+__global__ void __launch_bounds__(32 * kRowWarps) imm_row_kernel(const __grid_constant__ Args p, int parts) {
+  __shared__ int sums[kRowWarps][4 * M];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quads = kRowWarps / parts, quad = warp / parts, part = warp - quad * parts;
+  const int ch0 = (blockIdx.x * quads + quad) * 4;
+  const int chunks = p.k >> 4;
+  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * part / parts);
+  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (part + 1) / parts);
+  const int8_t* w[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) w[r] = p.w + static_cast<int64_t>(min(ch0 + r, p.n - 1)) * p.k;
+  if (lane < 4 && c1 > c0)                     // a hint: it may precede the wait for the previous kernel
+    prefetch_l2(w[lane] + 16 * c0, static_cast<uint32_t>(min((c1 - c0) * 16, 2048)));
+  grid_dependency_sync();
+  constexpr int kAhead = M == 1 ? 4 : M == 2 ? 2 : 1;   // rounds in flight, as the registers allow
+  int acc[4][M];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int t = 0; t < M; ++t) acc[r][t] = 0;
+#pragma unroll kAhead
+  for (int c = c0 + lane; c < c1; c += 32) {
+    uint4 x[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = ldg_stream(reinterpret_cast<const uint4*>(w[r]) + c);
+#pragma unroll
+    for (int t = 0; t < M; ++t) {
+      const int4 a = __ldg(reinterpret_cast<const int4*>(p.a + static_cast<int64_t>(min(t, p.m - 1)) * p.k) + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[r][t] = __dp4a(static_cast<int>(x[r].x), a.x, acc[r][t]);
+        acc[r][t] = __dp4a(static_cast<int>(x[r].y), a.y, acc[r][t]);
+        acc[r][t] = __dp4a(static_cast<int>(x[r].z), a.z, acc[r][t]);
+        acc[r][t] = __dp4a(static_cast<int>(x[r].w), a.w, acc[r][t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int t = 0; t < M; ++t) {
+      const int s = __reduce_add_sync(0xffffffffu, acc[r][t]);
+      if (lane == 0) sums[warp][r * M + t] = s;
+    }
+  __syncthreads();
+  if (threadIdx.x < quads * 4 * M) {
+    const int q = threadIdx.x / (4 * M), i = threadIdx.x - q * 4 * M, t = i % M;
+    const int ch = (blockIdx.x * quads + q) * 4 + i / M;
+    int sum = 0;
+    for (int s = 0; s < parts; ++s) sum += sums[q * parts + s][i];
+    if (ch < p.n && t < p.m)
+      store_one<OUT_BF16>(p.out, static_cast<int64_t>(t) * p.n + ch,
+                          finish(scaled(sum, p.sa[t]), p.sw[ch], p.bias != nullptr, p.bias != nullptr ? p.bias[ch] : 0.f));
+  }
 }
 
 // ------------------------------------------------------------- few tokens

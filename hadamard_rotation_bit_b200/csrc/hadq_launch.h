@@ -111,8 +111,10 @@ struct NormRingVariant {
 NormRingVariant norm_ring_for(bool bf16, bool residual, int64_t n);
 int norm_fault_bits(int clear);
 
-// int8 matrix product: the kernel for few tokens (up to `tokens` per CTA) and
-// the one for many.
+// int8 matrix product: the kernel for up to 4 tokens (imm::kRowWarps warps), the
+// one for few (up to `tokens` per CTA) and the one for many.
+using ImmRowFn = void (*)(const imm::Args, int);
+ImmRowFn imm_row_for(int64_t m, bool out_bf16);
 using ImmSplitFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args, int, int);
 using ImmPairFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args);
 struct ImmSplitVariant {

@@ -15,6 +15,12 @@ ImmSplitVariant split(bool out_bf16) {
 
 }  // namespace
 
+ImmRowFn imm_row_for(int64_t m, bool out_bf16) {
+  if (m == 1) return out_bf16 ? &imm::imm_row_kernel<1, true> : &imm::imm_row_kernel<1, false>;
+  if (m == 2) return out_bf16 ? &imm::imm_row_kernel<2, true> : &imm::imm_row_kernel<2, false>;
+  return out_bf16 ? &imm::imm_row_kernel<4, true> : &imm::imm_row_kernel<4, false>;
+}
+
 ImmSplitVariant imm_split_for(int64_t m, bool out_bf16) {
   if (m <= 16) return split<16, 5>(out_bf16);
   if (m <= 32) return split<32, 4>(out_bf16);

@@ -143,7 +143,7 @@ def check_matmul(out, a, sa, w, sw, bias):
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 128, 4096), (1, 4096, 14336), (2, 129, 48), (3, 7, 144), (5, 333, 112),
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 128, 4096), (4, 131, 14336), (3, 515, 4096), (2, 40, 16), (1, 4096, 14336), (2, 129, 48), (3, 7, 144), (5, 333, 112),
                                    (8, 4096, 512), (9, 200, 1040), (16, 1000, 4112), (17, 256, 128), (32, 512, 272),
                                    (33, 130, 96), (48, 1433, 4096), (64, 384, 1040), (65, 96, 208), (127, 255, 256),
                                    (128, 256, 64), (129, 257, 80), (200, 1024, 4096), (256, 128, 2048), (257, 511, 640),
