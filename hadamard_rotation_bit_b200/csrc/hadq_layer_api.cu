@@ -143,6 +143,7 @@ hadq_status check_cache_shape(const Cache& c) {
   if (c.page_size > kMaxDim || c.num_pages > kMaxDim || c.num_pages * c.page_size > INT32_MAX)
     return unsupported("the cache must hold fewer than 2^31 positions");
   if (c.kv_heads > 65536) return unsupported("at most 65536 K/V heads");
+  if (c.num_pages * c.page_size / 16 * c.kv_heads > UINT32_MAX - 1) return unsupported("the cache is larger than any device's memory");
   return HADQ_OK;
 }
 
@@ -240,12 +241,13 @@ hadq_status hadq_rmsnorm_quant(const void* x, hadq_dtype x_dtype, int64_t rows, 
       if (overlaps(outs[2], outs[0]) || overlaps(outs[2], outs[1])) return invalid("outputs must not overlap");
     }
     int stages = 0;
-    if (norm_takes_ring(rows, n, n * esize(x_dtype) * (residual ? 2 : 1), &stages)) {
+    const int64_t row_in = n * esize(x_dtype) * (residual ? 2 : 1);
+    if (norm_takes_ring(rows, n, row_in, &stages)) {
       const hl::NormRingVariant v = hl::norm_ring_for(x_dtype == HADQ_BF16, residual != nullptr, n);
       int sms = 0, dev = 0, occ = 0;
       st = device_sms(&sms, &dev);
       if (st != HADQ_OK) return st;
-      const int smem = static_cast<int>(stages * n * esize(x_dtype) * (residual ? 2 : 1));
+      const int smem = static_cast<int>(stages * row_in);
       st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, smem, &occ);
       if (st != HADQ_OK) return st;
       return launch_result(launch_pdl(v.fn, std::min<int64_t>(rows, int64_t(sms) * occ), v.threads, smem,

@@ -360,9 +360,12 @@ HADQ_API hadq_status hadq_kv4_append(const void* k, int64_t k_stride, const void
  *              of device memory (null when that is 0), written and read by
  *              this call: calls that may run at the same time need one each
  * Positions beyond a length are never read as numbers: any bits may lie there.
- * Scores, sums and the output accumulate in fp32; q (scaled by a power of 2)
- * and the probabilities are rounded to fp16 for the products, whose other side,
- * the codes, is exact.  Results do not depend on the order of execution.
+ * The codes enter the products exactly.  q R is rounded for them: with one
+ * scale per row (group = head_dim) to 16 bits below the largest value of its
+ * tile of 8 or 16 query rows (2^-15 of it, summed exactly in integers), with
+ * more to fp16 (2^-11 of each value); probabilities to fp16 (2^-11).  Maxima,
+ * sums and the output are held in fp32.  Results do not depend on the order of
+ * execution.
  */
 HADQ_API hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype, int64_t batch,
                                         int64_t q_len, int64_t heads, int64_t kv_heads, int64_t head_dim,

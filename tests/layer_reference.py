@@ -78,13 +78,16 @@ def cached_rows(codes, scales, pages, n):
 def attention(q, cache, table, lengths, scale, rotate):
     """(out, tolerance) in 64 bits: q [batch, q_len, heads, d].
 
-    The bound: a score is off by at most e = scale 2^-11 sum |q_d k_d| (q to
-    fp16; the fp32 sums of at most 128 products add less than 2^-16 of that
-    sum, taken as 2^-15 of the same), so p by a factor exp(+-e) in numerator
-    and denominator each; P is rounded to fp16 (2^-11) or, below 2^-14, by at
-    most 2^-25 per position against codes of at most 8 in units of the scale
-    of the position that leads the running maximum; exp2 and the fp32 sums
-    take another 2^-14; the result is rounded to bf16.
+    The bound: the rotated q is rounded to 2^-15 of the largest value of its
+    tile's rows (taken over all rows that share the K/V head) where a row has
+    one scale, so a score is off by at most scale 2^-15 max|q| sum |k_d|; with
+    more scales to fp16, off by 2^-11 per value, scale 2^-11 sum |q_d k_d|.
+    The fp32 rotation and sums of at most 128 products add less than 2^-16 of
+    sum |q_d k_d|, taken as 2^-15 of it.  With e the whole, p is off by a factor
+    exp(+-e) in numerator and denominator each; P is rounded to fp16 (2^-11)
+    or, below 2^-14, by at most 2^-25 per position against codes of at most 8
+    in units of the scale of the position that leads the running maximum; exp2
+    and the fp32 sums take another 2^-14; the result is rounded to bf16.
     """
     k_codes, k_scales, v_codes, v_scales = cache
     page = k_codes.shape[2]
@@ -93,6 +96,7 @@ def attention(q, cache, table, lengths, scale, rotate):
     ratio = heads // kv_heads
     out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
     tol = torch.zeros_like(out)
+    one_scale = k_scales.shape[3] == 1
     rot = torch.from_numpy(hadamard(d) / math.sqrt(d)).to(q.device)
     for b in range(batch):
         n = int(lengths[b])
@@ -101,17 +105,22 @@ def attention(q, cache, table, lengths, scale, rotate):
             continue
         k = cached_rows(k_codes, k_scales, pages, n).repeat_interleave(ratio, 0)      # [heads, n, d]
         v = cached_rows(v_codes, v_scales, pages, n).repeat_interleave(ratio, 0)
+        rows = q[b].double() @ rot if rotate else q[b].double()                      # [q_len, heads, d]
+        largest = rows.abs().amax((0, 2)).view(kv_heads, ratio).amax(1).repeat_interleave(ratio)
         sv = v_scales[pages].transpose(0, 1).flatten(1, 2)[:, :n].double().abs().amax((1, 2)).repeat_interleave(ratio, 0)
         for i in range(q_len):
             m = n - q_len + i + 1
             if m <= 0:
                 continue
-            row = q[b, i].double()
-            if rotate:
-                row = row @ rot
+            row = rows[i]
             p = torch.softmax(scale * torch.einsum("hd,hmd->hm", row, k[:, :m]), -1)
             y = torch.einsum("hm,hmd->hd", p, v[:, :m])
-            e = abs(scale) * (2.0 ** -11 + 2.0 ** -15) * torch.einsum("hd,hmd->hm", row.abs(), k[:, :m].abs()).amax(-1)
+            products = torch.einsum("hd,hmd->hm", row.abs(), k[:, :m].abs())
+            if one_scale:
+                e = 2.0 ** -15 * (products + largest[:, None] * k[:, :m].abs().sum(-1))
+            else:
+                e = (2.0 ** -15 + 2.0 ** -11) * products
+            e = abs(scale) * e.amax(-1)
             spread = torch.einsum("hm,hmd->hd", p, v[:, :m].abs())
             out[b, i] = y
             tol[b, i] = (y.abs() * HALF[torch.bfloat16]

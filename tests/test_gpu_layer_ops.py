@@ -110,10 +110,11 @@ def test_norm_small_and_large_rows(size):
 
 
 @pytest.mark.parametrize("target", ["x", "residual"])
-def test_norm_in_place(target):
+@pytest.mark.parametrize("rows,n", [(64, 4096), (5000, 4096), (1100, 14336)])
+def test_norm_in_place(rows, n, target):
     g = gen(5)
-    x, r = randn(g, 64, 4096, dtype=torch.bfloat16), randn(g, 64, 4096, dtype=torch.bfloat16)
-    w = randn(g, 4096, dtype=torch.bfloat16)
+    x, r = randn(g, rows, n, dtype=torch.bfloat16), randn(g, rows, n, dtype=torch.bfloat16)
+    w = randn(g, n, dtype=torch.bfloat16)
     x0, r0 = x.clone(), r.clone()
     codes, scales, stream = H.hadq_rmsnorm_quant(x, w, residual=r, residual_out=x if target == "x" else r)
     assert stream.data_ptr() == (x if target == "x" else r).data_ptr()

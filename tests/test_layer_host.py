@@ -74,7 +74,7 @@ def append(lib, k=at(1), ks=512, v=at(2), vs=512, dt=1, tokens=3, heads=4, d=128
 CACHE_BAD = [
     (dict(heads=0), INV), (dict(pages=0), INV), (dict(page=0), INV), (dict(page=24), UNS), (dict(page=8), UNS),
     (dict(d=96, group=32), UNS), (dict(d=256), UNS), (dict(group=48), INV), (dict(d=64, group=128), INV), (dict(block=64), UNS),
-    (dict(block=2), UNS), (dict(block=-2), UNS), (dict(pages=1 << 27, page=16), UNS), (dict(pages=1 << 40), UNS),
+    (dict(block=2), UNS), (dict(block=-2), UNS), (dict(pages=1 << 27, page=16), UNS), (dict(pages=1 << 40), UNS), (dict(pages=1 << 26, heads=32768), UNS),
     (dict(cache=(None, *CACHE[1:])), INV), (dict(cache=(*CACHE[:3], None)), INV),
     (dict(cache=(CACHE[0] + 8, *CACHE[1:])), MIS), (dict(cache=(*CACHE[:3], CACHE[3] + 2)), MIS),
     (dict(cache=(CACHE[0], CACHE[1], CACHE[0] + 64, CACHE[3])), INV)]
