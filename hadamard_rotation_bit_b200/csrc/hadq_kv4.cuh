@@ -904,64 +904,73 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   }
 }
 
-// Adds the splits' parts, one CTA per unit: two warps a row, each its half of
-// the splits in order.
+// Adds the splits' parts, one CTA per unit: one to kPieces warps a row
+// (blockDim.x), each its share of the splits in order, then the shares in order.
+template <int ROWS>
+constexpr int kPieces = ROWS == 8 ? 4 : 2;
+
 template <int D, int ROWS>
-__global__ void __launch_bounds__(64 * ROWS) kv4_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * ROWS * kPieces<ROWS>, 1) kv4_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int E = D / 32;
-  __shared__ float part[ROWS][D + 2];
+  __shared__ float part[kPieces<ROWS>][ROWS][D];
+  __shared__ float2 part_ml[kPieces<ROWS>][ROWS];
   grid_dependency_sync();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = warp % ROWS, half = warp / ROWS;
+  const int row = warp % ROWS, piece = warp / ROWS, pieces = blockDim.x / (32 * ROWS);
   const int unit = blockIdx.x;
   const int bh = static_cast<int>(a.row_tiles(unit)), rt = unit - bh * a.row_tiles.d;
   const int b = static_cast<int>(a.kv_heads(bh)), h = bh - b * a.kv_heads.d;
   const int ratio = a.ratio.d, rho = rt * ROWS + row, qi = static_cast<int>(a.ratio(rho));
   const bool live = rho < a.q_len * ratio;
+  const int s0 = a.splits * piece / pieces, s1 = live ? a.splits * (piece + 1) / pieces : s0;
   auto part_row = [&](int s) { return (static_cast<int64_t>(s) * a.units + unit) * ROWS + row; };
   float top = -1.0e30f;
-  if (live)
-    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[part_row(s)].x);
+  for (int s = s0 + lane; s < s1; s += 32) top = fmaxf(top, a.part_ml[part_row(s)].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   float sum = 0.f, v[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) v[i] = 0.f;
-  const int mid = a.splits >> 1;
-  if (live) {
 #pragma unroll 8
-    for (int s = half ? mid : 0; s < (half ? a.splits : mid); ++s) {
-      const int64_t r = part_row(s);
-      const float2 ml = a.part_ml[r];
-      const float f = exp2_fast(ml.x - top);
-      const float* p = a.part_o + r * D + lane * E;
-      float y[E];
-      if constexpr (E == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
-        y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        y[0] = x.x, y[1] = x.y;
-      }
-      sum = fmaf(ml.y, f, sum);
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = ml.y > 0.f ? fmaf(y[i], f, v[i]) : v[i];   // an empty part was not written
+  for (int s = s0; s < s1; ++s) {
+    const int64_t r = part_row(s);
+    const float2 ml = a.part_ml[r];
+    const float f = exp2_fast(ml.x - top);
+    const float* p = a.part_o + r * D + lane * E;
+    float y[E];
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(p);
+      y[0] = x.x, y[1] = x.y;
     }
-  }
-  if (half == 1) {
+    sum = fmaf(ml.y, f, sum);
 #pragma unroll
-    for (int i = 0; i < E; ++i) part[row][lane * E + i] = v[i];
-    if (lane == 0) part[row][D] = sum;
+    for (int i = 0; i < E; ++i) v[i] = ml.y > 0.f ? fmaf(y[i], f, v[i]) : v[i];   // an empty part was not written
   }
+#pragma unroll
+  for (int i = 0; i < E; ++i) part[piece][row][lane * E + i] = v[i];
+  if (lane == 0) part_ml[piece][row] = make_float2(top, sum);
   __syncthreads();
-  if (half == 1 || !live) return;
-  sum += part[row][D];
+  if (piece != 0 || !live) return;
+  float all = -1.0e30f;
+  for (int i = 0; i < pieces; ++i) all = fmaxf(all, part_ml[i][row].x);
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] = 0.f;
+  for (int q = 0; q < pieces; ++q) {
+    const float2 ml = part_ml[q][row];
+    const float f = exp2_fast(ml.x - all);
+    sum = fmaf(ml.y, f, sum);
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = fmaf(part[q][row][lane * E + i], f, v[i]);
+  }
   const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
   const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads.d * ratio) + h * ratio + rho - qi * ratio;
 #pragma unroll
   for (int i = 0; i < E; i += 2)
-    *reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E + i) =
-        pack_bf16x2((v[i] + part[row][lane * E + i]) * inv, (v[i + 1] + part[row][lane * E + i + 1]) * inv);
+    *reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E + i) = pack_bf16x2(v[i] * inv, v[i + 1] * inv);
 }
 
 }  // namespace kv4

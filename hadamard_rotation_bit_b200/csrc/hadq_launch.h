@@ -131,12 +131,12 @@ int imm_fault_bits(int clear);
 
 // int4 cache: append, and attention for `rows` query rows per K/V head: the
 // kernel (variant.rows of them per CTA, variant.ctas CTAs at once on an SM) and
-// the join of its splits.
+// the join of its splits (at most `pieces` warps a row).
 using AppendFn = void (*)(const kv4::AppendArgs);
 using AttnFn = void (*)(const kv4::AttnArgs);
 struct AttnVariant {
   AttnFn fn, join;
-  int threads, smem, rows, ctas;
+  int threads, smem, rows, ctas, pieces;
 };
 AppendFn kv4_append_for(bool bf16, int d);
 AttnVariant kv4_attention_for(int d, int group, int rows);

@@ -191,8 +191,8 @@ hadq_status check_attention_shape(int64_t batch, int64_t q_len, int64_t heads, i
 // Splits of a sequence over CTAs, from sizes alone, so that a captured call and
 // its workspace hold for any lengths: about 1.75 CTAs for each that fits the GPU
 // at once (512 units: 60.7 us with 2 splits, 64.3 with 1, 64.4 with 3), but at
-// least 32 steps of 32 positions for a CTA (8 units of 32768 positions: 19.4 us
-// with 32 splits, 20.6 with 18, 23.8 with 64).
+// least 32 steps of 32 positions for a CTA (8 units of 32768 positions: 15.7 us
+// with 32 splits, 17.9 with 16, 18.5 with 42, 19.3 with 64).
 int attention_splits(const hl::AttnVariant& v, int64_t units, int64_t max_positions) {
   const int64_t slots = 148 * v.ctas, steps = ceil_div(max_positions, 32);
   const int64_t want = (7 * slots + 2 * units) / (4 * units);
@@ -432,7 +432,8 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
     st = launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(units), static_cast<unsigned>(splits)), 1, v.threads, v.smem, s, p),
                        "cache attention launch");
     if (st != HADQ_OK || splits == 1) return st;
-    return launch_result(launch_pdl(v.join, units, 64 * v.rows, 0, s, p), "cache attention join launch");
+    const int pieces = static_cast<int>(std::min<int64_t>(v.pieces, ceil_div(splits, 8)));   // 8 parts in flight a warp
+    return launch_result(launch_pdl(v.join, units, 32 * v.rows * pieces, 0, s, p), "cache attention join launch");
   });
 }
 

@@ -11,7 +11,7 @@ template <int D, int GROUP, int NT>
 AttnVariant attn() {
   using C = kv4::Cfg<D, GROUP, NT, 3>;
   return AttnVariant{&kv4::kv4_attention_kernel<D, GROUP, NT, 3>, &kv4::kv4_join_kernel<D, C::ROWS>, 32 * kv4::kWarps,
-                     C::SMEM_BYTES, C::ROWS, NT == 1 ? 4 : 2};
+                     C::SMEM_BYTES, C::ROWS, NT == 1 ? 4 : 2, kv4::kPieces<C::ROWS>};
 }
 
 template <int D, int GROUP>
@@ -30,7 +30,7 @@ AttnVariant kv4_attention_for(int d, int group, int rows) {
     if (group == 64) return attn_rows<64, 64>(rows);
     if (group == 32) return attn_rows<64, 32>(rows);
   }
-  return AttnVariant{nullptr, nullptr, 0, 0, 0, 0};
+  return AttnVariant{nullptr, nullptr, 0, 0, 0, 0, 0};
 }
 
 AppendFn kv4_append_for(bool bf16, int d) {
