@@ -189,14 +189,21 @@ hadq_status check_attention_shape(int64_t batch, int64_t q_len, int64_t heads, i
 }
 
 // Splits of a sequence over CTAs, from sizes alone, so that a captured call and
-// its workspace hold for any lengths: about 1.75 CTAs for each that fits the GPU
-// at once (512 units: 60.7 us with 2 splits, 64.3 with 1, 64.4 with 3), but at
-// least 32 steps of 32 positions for a CTA (8 units of 32768 positions: 15.7 us
-// with 32 splits, 17.9 with 16, 18.5 with 42, 19.3 with 64).
+// its workspace hold for any lengths.  Few units: 256 CTAs, under two to an SM (a
+// grid that just fills two leaves some SMs with three), as long as each of their
+// warps has a step of 32 positions, but no more than 32 splits (the join then
+// takes one round), or twice that where it leaves a warp more than 16 steps.
+// (Device us, 8 units: 32768 positions 14.2 with 32 splits, 16.4 with 37, 17.3
+// with 16; 8192 positions 8.2, 9.6, 8.4; 131072 positions 36.0 with 64, 43.5 with
+// 37.  32 units of 8192: 13.8 with 8 splits, 16.2 with 9.)
+// Many: about 1.75 for each CTA that fits the GPU at once, so that a second,
+// shorter round evens out unequal lengths (512 units of 4096: 60.7 us with 2
+// splits, 64.3 with 1, 64.4 with 3).
 int attention_splits(const hl::AttnVariant& v, int64_t units, int64_t max_positions) {
-  const int64_t slots = 148 * v.ctas, steps = ceil_div(max_positions, 32);
-  const int64_t want = (7 * slots + 2 * units) / (4 * units);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, steps / 32)));
+  const int64_t slots = 148 * v.ctas, steps = ceil_div(max_positions, 32), some = std::max<int64_t>(units, 1);
+  int64_t want = (7 * slots + 2 * some) / (4 * some);
+  if (some <= 256) want = steps <= 64 * 32 ? std::min<int64_t>(256 / some, 32) : std::min<int64_t>(512 / some, 64);
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, steps / 4)));
 }
 
 int64_t attention_units(const hl::AttnVariant& v, int64_t batch, int64_t rows, int64_t kv_heads) {
