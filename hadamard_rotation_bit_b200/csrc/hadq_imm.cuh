@@ -6,15 +6,20 @@
 // memory).  The sums are exact for k < 131072, so their order is free: a split
 // of k adds up to the same bits, and every kernel here gives the same result.
 //
-// Three kernels.
+// Four kernels.
 //
 //   imm_row_kernel    a handful of tokens: bound by reading w, and by what it
 //       takes to begin.  Warps read rows of w straight from global memory and
 //       form four-way byte products; nothing is set up first.  4096 x 14336: 9.5
 //       us with 1 token (6.2 TB/s), 10.4 with 4, against 13.6 and 13.8 of the
-//       next kernel; with 8 tokens 17.3 against 13.8, the byte products'
+//       split kernel; with 8 tokens 17.3 against 13.8, the byte products'
 //       operands no longer fit beside the loads.
-//   imm_split_kernel  few tokens: bound by reading w.  Output channels are the
+//   imm_warp_kernel   up to 16 tokens: the same, with the warps' matrix
+//       instructions.  8 and 16 tokens, 4096 x 4096: 4.7 and 4.9 us against 6.5
+//       and 6.5 of the split kernel; 4096 x 14336: 13.0 and 13.1 against 13.7
+//       and 13.7.  From 32 tokens on the token loads of every warp cost more
+//       (8.4 against 7.4).
+//   imm_split_kernel  up to a few hundred tokens: bound by reading w.  Output channels are the
 //       MMA's 128 rows and TN tokens its columns, so one token costs no more
 //       traffic than it has, and the CTAs of a cluster share the k of a tile,
 //       adding their sums through distributed shared memory.
@@ -197,6 +202,106 @@ __global__ void __launch_bounds__(32 * kRowWarps) imm_row_kernel(const __grid_co
   }
 }
 
+// ------------------------------------------------------------ up to 16 tokens
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A warp takes 16 MT channels (the rows of its products), all 8 NT tokens (their
+// columns) and one of `parts` runs of k, 64 bytes at a time: lane (r, c) holds
+// bytes 16 c .. of channel rows r, r + 8 and of token r, which are the operands of
+// two products as they lie (the order of a contraction is free).  Weights come
+// straight from global memory, two rounds ahead; tokens, read by every warp,
+// through L1.  The warps' sums meet in shared memory, by integer atomics (exact
+// in any order).
+template <int MT, int NT, bool OUT_BF16>
+__global__ void __launch_bounds__(32 * kRowWarps, 2) imm_warp_kernel(const __grid_constant__ Args p, int parts) {
+  constexpr int CH = 16 * MT, TOK = 8 * NT;
+  extern __shared__ int sums[];                // [group of channels][token][CH]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int groups = kRowWarps / parts, group = warp / parts, part = warp - group * parts;
+  const int ch0 = (blockIdx.x * groups + group) * CH;
+  const int rounds = (p.k + 63) >> 6;
+  const int i0 = static_cast<int>(static_cast<int64_t>(rounds) * part / parts);
+  const int i1 = static_cast<int>(static_cast<int64_t>(rounds) * (part + 1) / parts);
+  if (lane < CH && i1 > i0 && ch0 + lane < p.n)  // a hint: it may precede the wait for the previous kernel
+    prefetch_l2(p.w + static_cast<int64_t>(ch0 + lane) * p.k + 64 * i0, static_cast<uint32_t>(min(min((i1 - i0) * 64, p.k - 64 * i0), 512)));
+  for (int i = threadIdx.x; i < groups * TOK * CH; i += 32 * kRowWarps) sums[i] = 0;
+  const int8_t* w[MT][2];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) w[t][e] = p.w + static_cast<int64_t>(min(ch0 + 16 * t + 8 * e + r, p.n - 1)) * p.k + 16 * c;
+  const int8_t* a[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) a[t] = p.a + static_cast<int64_t>(min(8 * t + r, p.m - 1)) * p.k + 16 * c;
+  __syncthreads();
+  grid_dependency_sync();
+
+  int acc[MT][NT][4];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[t][u][k] = 0;
+  uint4 x[2][MT][2];
+  auto load = [&](int i, uint4 (&y)[MT][2]) {  // zeros past the end of k
+    const bool in = i < i1 && 64 * i + 16 * c < p.k;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        y[t][e] = in ? ldg_stream(reinterpret_cast<const uint4*>(w[t][e] + 64 * i)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto step = [&](int i, uint4 (&y)[MT][2]) {
+    const int at = 64 * i + 16 * c < p.k ? 64 * i : 0;   // any bytes will do against zeros
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(a[u] + at));
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        mma_s8(acc[t][u], y[t][0].x, y[t][1].x, y[t][0].y, y[t][1].y, b.x, b.y);
+        mma_s8(acc[t][u], y[t][0].z, y[t][1].z, y[t][0].w, y[t][1].w, b.z, b.w);
+      }
+    }
+  };
+  load(i0, x[0]);
+  load(i0 + 1, x[1]);
+#pragma unroll 1
+  for (int i = i0; i < i1; i += 2) {
+    step(i, x[0]);
+    load(i + 2, x[0]);
+    if (i + 1 < i1) step(i + 1, x[1]);
+    load(i + 3, x[1]);
+  }
+  int* mine = sums + group * TOK * CH;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        int* at = mine + (8 * u + 2 * c + (k & 1)) * CH + 16 * t + 8 * (k >> 1) + r;
+        if (parts > 1) atomicAdd(at, acc[t][u][k]);
+        else *at = acc[t][u][k];
+      }
+  __syncthreads();
+  // channels along the lanes
+  for (int i = threadIdx.x; i < groups * CH * p.m; i += 32 * kRowWarps) {
+    const int col = i % (groups * CH), tok = i / (groups * CH), g = col / CH;
+    const int ch = blockIdx.x * groups * CH + col;
+    if (ch < p.n)
+      store_one<OUT_BF16>(p.out, static_cast<int64_t>(tok) * p.n + ch,
+                          finish(scaled(sums[(g * TOK + tok) * CH + col - g * CH], p.sa[tok]), p.sw[ch], p.bias != nullptr,
+                                 p.bias != nullptr ? p.bias[ch] : 0.f));
+  }
+}
+
 // ------------------------------------------------------------- few tokens
 
 template <int TN_, int STAGES_>
@@ -204,7 +309,8 @@ struct SplitCfg {
   static constexpr int TN = TN_, STAGES = STAGES_;
   static constexpr int W_BYTES = 128 * kSlice, A_BYTES = TN * kSlice;
   static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;
-  static constexpr int TMEM_COLS = TN < 32 ? 32 : TN;
+  static_assert(TN % 32 == 0, "a rank of up to 8 takes four columns or more");
+  static constexpr int TMEM_COLS = TN;
   static constexpr int THREADS = 128;
   static constexpr int SM_RING = 0;
   static constexpr int SM_JOIN = STAGES * STAGE_BYTES;                // [source rank][quad of columns][channel][4]
@@ -335,8 +441,8 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   } else {
     // Token column c goes to rank c / mine; there, the sources' sums are added
     // (integers: in any order the same).  Four columns of a channel travel
-    // together, or two where a rank has two.
-    const int mine = TN / splits, lg = __ffs(mine) - 1;   // 2 or more, a power of 2
+    // together.
+    const int mine = TN / splits, lg = __ffs(mine) - 1;   // 4 or more, a power of 2
     cluster_wait();
     const uint32_t join = smem_u32(smem + C::SM_JOIN);
 #pragma unroll 1
@@ -348,51 +454,30 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = 0;
       }
-      if (mine >= 4) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const uint32_t at = join + (((rank << lg) + ((c + j) & (mine - 1))) * 128 + threadIdx.x * 4) * 4;
-          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_rank(at, (c + j) >> lg)), "r"(v[j]),
-                       "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3])
-                       : "memory");
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const uint32_t at = join + (rank * 256 + threadIdx.x * 2) * 4;
-          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(map_rank(at, (c + j) >> 1)), "r"(v[j]), "r"(v[j + 1])
-                       : "memory");
-        }
+      for (int j = 0; j < 16; j += 4) {
+        const uint32_t at = join + (((rank << lg) + ((c + j) & (mine - 1))) * 128 + threadIdx.x * 4) * 4;
+        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_rank(at, (c + j) >> lg)), "r"(v[j]),
+                     "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3])
+                     : "memory");
       }
     }
     cluster_arrive();
     cluster_wait();
     const int* got = reinterpret_cast<const int*>(smem + C::SM_JOIN);
-    if (mine >= 4) {
 #pragma unroll 2
-      for (int col = 0; col < mine; col += 4) {
-        int4 sum = make_int4(0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < splits) {
-            const int4 x = *reinterpret_cast<const int4*>(got + ((r << lg) + col) * 128 + threadIdx.x * 4);
-            sum = make_int4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
-          }
-        put(rank * mine + col, sum.x);
-        put(rank * mine + col + 1, sum.y);
-        put(rank * mine + col + 2, sum.z);
-        put(rank * mine + col + 3, sum.w);
-      }
-    } else {
-      int2 sum = make_int2(0, 0);
+    for (int col = 0; col < mine; col += 4) {
+      int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < 8; ++r)
         if (r < splits) {
-          const int2 x = *reinterpret_cast<const int2*>(got + r * 256 + threadIdx.x * 2);
-          sum = make_int2(sum.x + x.x, sum.y + x.y);
+          const int4 x = *reinterpret_cast<const int4*>(got + ((r << lg) + col) * 128 + threadIdx.x * 4);
+          sum = make_int4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
         }
-      put(rank * 2, sum.x);
-      put(rank * 2 + 1, sum.y);
+      put(rank * mine + col, sum.x);
+      put(rank * mine + col + 1, sum.y);
+      put(rank * mine + col + 2, sum.z);
+      put(rank * mine + col + 3, sum.w);
     }
   }
   tc_fence_before();

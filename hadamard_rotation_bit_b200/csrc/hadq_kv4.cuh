@@ -523,7 +523,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     if (row < C::ROWS) qs[((row >> 3) * NG + w) * 32 + (row & 7) * 4 + qc] = x;
   }
   __syncthreads();
-  uint32_t qb[NT][NG][4];
+  uint4 qb[NT == 1 ? NG : 1];                 // one tile of rows: in registers; two: read at each use
+  auto query = [&](int nt, int w) { return NT == 1 ? qb[w] : qs[(nt * NG + w) * 32 + lane]; };
   float bias[NT][G][2];                       // G > 1: what the 8 in (code + 8) adds to a row's sums, negative
   int limit[NT][2];                           // first position that rows 2c, 2c + 1 do not see
 #pragma unroll
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 #pragma unroll
       for (int w = g * (GROUP / 32); w < (g + 1) * (GROUP / 32); ++w) {
         const uint4 x = qs[(nt * NG + w) * 32 + lane];
-        qb[nt][w][0] = x.x, qb[nt][w][1] = x.y, qb[nt][w][2] = x.z, qb[nt][w][3] = x.w;
+        if constexpr (NT == 1) qb[w] = x;
         if constexpr (G > 1) {
           mma16816(eight, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.x, x.y);
           mma16816(eight, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.z, x.w);
@@ -636,12 +637,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
             const uint32_t a1 = (kw[tt][1][w] << 4) & 0xF0F0F0F0u, a3 = kw[tt][1][w] & 0xF0F0F0F0u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              const uint4 q = query(nt, w);
               if (w == 0) {
-                mma16832_from0<true>(high[tt][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
-                mma16832_from0<false>(low[tt][nt], a0, a1, a2, a3, qb[nt][w][2], qb[nt][w][3]);
+                mma16832_from0<true>(high[tt][nt], a0, a1, a2, a3, q.x, q.y);
+                mma16832_from0<false>(low[tt][nt], a0, a1, a2, a3, q.z, q.w);
               } else {
-                mma16832<true>(high[tt][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
-                mma16832<false>(low[tt][nt], a0, a1, a2, a3, qb[nt][w][2], qb[nt][w][3]);
+                mma16832<true>(high[tt][nt], a0, a1, a2, a3, q.x, q.y);
+                mma16832<false>(low[tt][nt], a0, a1, a2, a3, q.z, q.w);
               }
             }
           }
@@ -668,8 +670,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
             const int gw = g * (GROUP / 32) + w;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816(acc[tt][nt], xa[0], xb[0], xa[1], xb[1], qb[nt][gw][0], qb[nt][gw][1]);
-              mma16816(acc[tt][nt], xa[2], xb[2], xa[3], xb[3], qb[nt][gw][2], qb[nt][gw][3]);
+              const uint4 q = query(nt, gw);
+              mma16816(acc[tt][nt], xa[0], xb[0], xa[1], xb[1], q.x, q.y);
+              mma16816(acc[tt][nt], xa[2], xb[2], xa[3], xb[3], q.z, q.w);
             }
           }
       }

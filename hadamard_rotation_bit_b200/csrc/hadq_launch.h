@@ -111,10 +111,15 @@ struct NormRingVariant {
 NormRingVariant norm_ring_for(bool bf16, bool residual, int64_t n);
 int norm_fault_bits(int clear);
 
-// int8 matrix product: the kernel for up to 4 tokens (imm::kRowWarps warps), the
-// one for few (up to `tokens` per CTA) and the one for many.
+// int8 matrix product: the kernels for up to 4 and 16 tokens (imm::kRowWarps
+// warps), the one for few (up to `tokens` per CTA) and the one for many.
 using ImmRowFn = void (*)(const imm::Args, int);
 ImmRowFn imm_row_for(int64_t m, bool out_bf16);
+struct ImmWarpVariant {
+  ImmRowFn fn;
+  int channels, tokens;   // of a warp
+};
+ImmWarpVariant imm_warp_for(int64_t m, bool two, bool out_bf16);   // m <= 16; two: 32 channels a warp
 using ImmSplitFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args, int, int);
 using ImmPairFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args);
 struct ImmSplitVariant {

@@ -21,8 +21,22 @@ ImmRowFn imm_row_for(int64_t m, bool out_bf16) {
   return out_bf16 ? &imm::imm_row_kernel<4, true> : &imm::imm_row_kernel<4, false>;
 }
 
+namespace {
+
+template <int MT>
+ImmWarpVariant warp_variant(int64_t m, bool out_bf16) {
+  auto v = [&](auto bf16, auto f32, int nt) { return ImmWarpVariant{out_bf16 ? bf16 : f32, 16 * MT, 8 * nt}; };
+  if (m <= 8) return v(&imm::imm_warp_kernel<MT, 1, true>, &imm::imm_warp_kernel<MT, 1, false>, 1);
+  return v(&imm::imm_warp_kernel<MT, 2, true>, &imm::imm_warp_kernel<MT, 2, false>, 2);
+}
+
+}  // namespace
+
+ImmWarpVariant imm_warp_for(int64_t m, bool two, bool out_bf16) {
+  return two ? warp_variant<2>(m, out_bf16) : warp_variant<1>(m, out_bf16);
+}
+
 ImmSplitVariant imm_split_for(int64_t m, bool out_bf16) {
-  if (m <= 16) return split<16, 5>(out_bf16);
   if (m <= 32) return split<32, 4>(out_bf16);
   if (m <= 64) return split<64, 6>(out_bf16);
   return split<128, 4>(out_bf16);

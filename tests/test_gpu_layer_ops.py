@@ -145,7 +145,7 @@ def check_matmul(out, a, sa, w, sw, bias):
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 128, 4096), (4, 131, 14336), (3, 515, 4096), (2, 40, 16), (1, 4096, 14336), (2, 129, 48), (3, 7, 144), (5, 333, 112),
-                                   (8, 4096, 512), (9, 200, 1040), (16, 1000, 4112), (17, 256, 128), (32, 512, 272),
+                                   (8, 4096, 512), (5, 9001, 80), (8, 8200, 4112), (13, 8193, 1040), (7, 33, 16), (16, 4096, 14336), (9, 200, 1040), (16, 1000, 4112), (17, 256, 128), (32, 512, 272),
                                    (33, 130, 96), (48, 1433, 4096), (64, 384, 1040), (65, 96, 208), (127, 255, 256),
                                    (128, 256, 64), (129, 257, 80), (200, 1024, 4096), (256, 128, 2048), (257, 511, 640),
                                    (333, 1001, 4112), (512, 4096, 1024), (1025, 520, 384), (2000, 24, 256),
@@ -163,7 +163,7 @@ def test_matmul(m, n, k, out):
     check()
 
 
-@pytest.mark.parametrize("m,n", [(1, 130), (17, 65), (200, 300)])
+@pytest.mark.parametrize("m,n", [(1, 130), (3, 33), (9, 40), (17, 65), (200, 300)])
 def test_matmul_largest_sums(m, n):
     """-128 x -128 over the longest k: 2147221504, just inside 32 bits."""
     k = 131056
@@ -189,7 +189,7 @@ def test_matmul_leading_dimensions_zero_scales_and_empty():
 
 def test_matmul_same_result_every_time():
     g = gen(10)
-    for m in (1, 24, 300):
+    for m in (1, 4, 12, 24, 300):
         a = torch.randint(-127, 128, (m, 14336), generator=g, device="cuda", dtype=torch.int8)
         w = torch.randint(-127, 128, (1024, 14336), generator=g, device="cuda", dtype=torch.int8)
         sa, sw = torch.rand(m, device="cuda"), torch.rand(1024, device="cuda")
