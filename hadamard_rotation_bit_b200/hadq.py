@@ -14,6 +14,7 @@ fails, a ``HadqError`` is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -497,10 +498,10 @@ def hadq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     include/hadq.h).  Returns (codes, scales, residual_out); the last is
     x + residual, or None without a residual.  residual_out may be x or residual."""
     lib = _lib or load_library()
-    rows, n = _rows_n(x)
     dev, dtype, shape = x.get_device(), x.dtype, x.shape
-    lead = shape[:-1]
     xp = _takes("x", x, dev, dtype, shape)
+    lead, n = shape[:-1], shape[-1] if shape else 1
+    rows = x.numel() // n if n else 0
     wp = _takes("weight", weight, dev, dtype, (n,))
     rp = op = None
     if residual is not None:
@@ -532,9 +533,10 @@ def hadq_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
     """(a . w^T) * a_scales[:, None] * w_scales + bias of int8 codes a [..., k]
     and weights w [cols, k] (see include/hadq.h)."""
     lib = _lib or load_library()
-    rows, k = _rows_n(a)
-    dev, lead = a.get_device(), a.shape[:-1]
-    ap = _takes("a", a, dev, torch.int8, a.shape)
+    dev, shape = a.get_device(), a.shape
+    ap = _takes("a", a, dev, torch.int8, shape)
+    lead, k = shape[:-1], shape[-1] if shape else 1
+    rows = a.numel() // k if k else 0
     asp = _takes("a_scales", a_scales, dev, torch.float32, lead)
     cols = w.shape[0] if w.dim() else 0
     wp = _takes("w", w, dev, torch.int8, (cols, k))
@@ -604,6 +606,12 @@ def hadq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cod
           size, *ptrs)
 
 
+@functools.lru_cache(maxsize=1024)
+def _kv4_workspace(*sizes: int) -> int:
+    """Bytes for these sizes, -1 where the call refuses them."""
+    return int(load_library().hadq_kv4_attention_workspace(*sizes))
+
+
 def hadq_kv4_attention_workspace(batch: int, q_len: int, heads: int, kv_heads: int, head_dim: int,
                                  max_positions: int) -> int:
     """Bytes of hadq_kv4_attention's workspace (see include/hadq.h)."""
@@ -639,7 +647,7 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
         op = _takes("out", out, dev, dtype, shape)
     nbytes, ws = 0, None
     if workspace is None:
-        need = lib.hadq_kv4_attention_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
+        need = _kv4_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
         if need > 0:
             workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None:
