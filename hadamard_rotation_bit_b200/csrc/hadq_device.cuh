@@ -191,6 +191,21 @@ __device__ __forceinline__ void ldg_stream32(const void* p, uint4& a, uint4& b) 
                : "l"(p));
 }
 
+// The same without the read-only path, for data that the previous kernel of the
+// stream may still be writing when this one starts (before the wait for it).
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ void ld_stream32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p) : "memory");
+}
+
 // NE contiguous input elements starting at element index e -> dst[0..NE).
 // A thread's run is far from its neighbours' (a segment or a team chunk), so
 // a 16-byte load uses half of each 32-byte sector it fetches and the next

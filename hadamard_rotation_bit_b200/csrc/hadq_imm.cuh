@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) imm_row_kernel(const __grid_co
   for (int c = c0 + lane; c < c1; c += 32) {
     uint4 x[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = ldg_stream(reinterpret_cast<const uint4*>(w[r]) + c);
+    for (int r = 0; r < 4; ++r) x[r] = ld_stream(reinterpret_cast<const uint4*>(w[r]) + c);
 #pragma unroll
     for (int t = 0; t < M; ++t) {
-      const int4 a = __ldg(reinterpret_cast<const int4*>(p.a + static_cast<int64_t>(min(t, p.m - 1)) * p.k) + c);
+      const int4 a = reinterpret_cast<const int4*>(p.a + static_cast<int64_t>(min(t, p.m - 1)) * p.k)[c];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         acc[r][t] = __dp4a(static_cast<int>(x[r].x), a.x, acc[r][t]);
@@ -256,13 +256,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) imm_warp_kernel(const __gri
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        y[t][e] = in ? ldg_stream(reinterpret_cast<const uint4*>(w[t][e] + 64 * i)) : make_uint4(0u, 0u, 0u, 0u);
+        y[t][e] = in ? ld_stream(reinterpret_cast<const uint4*>(w[t][e] + 64 * i)) : make_uint4(0u, 0u, 0u, 0u);
   };
   auto step = [&](int i, uint4 (&y)[MT][2]) {
     const int at = 64 * i + 16 * c < p.k ? 64 * i : 0;   // any bytes will do against zeros
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(a[u] + at));
+      const uint4 b = *reinterpret_cast<const uint4*>(a[u] + at);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         mma_s8(acc[t][u], y[t][0].x, y[t][1].x, y[t][0].y, y[t][1].y, b.x, b.y);

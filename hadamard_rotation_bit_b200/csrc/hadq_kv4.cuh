@@ -66,6 +66,34 @@ struct AppendArgs {
   float norm;                // fp32(1 / sqrt(D))
 };
 
+// 32 consecutive values: 256-bit loads where they are 32-byte aligned (whole
+// sectors), else 128-bit ones.
+template <bool BF16>
+__device__ __forceinline__ void load32(const void* x, int64_t e, float (&v)[32]) {
+  constexpr int N = BF16 ? 4 : 8;
+  const uint8_t* p = static_cast<const uint8_t*>(x) + e * (BF16 ? 2 : 4);
+  uint4 w[N];
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) ld_stream32(p + 16 * i, w[i], w[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (BF16) {
+      unpack_bf16x2(w[i].x, v[8 * i + 0], v[8 * i + 1]);
+      unpack_bf16x2(w[i].y, v[8 * i + 2], v[8 * i + 3]);
+      unpack_bf16x2(w[i].z, v[8 * i + 4], v[8 * i + 5]);
+      unpack_bf16x2(w[i].w, v[8 * i + 6], v[8 * i + 7]);
+    } else {
+      v[4 * i] = __uint_as_float(w[i].x), v[4 * i + 1] = __uint_as_float(w[i].y);
+      v[4 * i + 2] = __uint_as_float(w[i].z), v[4 * i + 3] = __uint_as_float(w[i].w);
+    }
+  }
+}
+
 // Even CTAs store K, odd ones V, side by side: one computes, the other copies.
 // Five CTAs an SM hide the loads (32768 tokens x 8 heads x 128: 38.3 us, 4.4
 // TB/s; 41 with four, 43.3 with resident CTAs that load ahead into registers).
@@ -83,7 +111,7 @@ __global__ void __launch_bounds__(256, 5) kv4_append_kernel(const __grid_constan
   const int64_t slot = live ? a.slots[token] : -1;
   float v[32];
   if (live) {
-    load_elems<BF16, 32>(a.x[which], static_cast<int64_t>(token) * a.stride[which] + static_cast<int64_t>(head) * D + part * 32, v);
+    load32<BF16>(a.x[which], static_cast<int64_t>(token) * a.stride[which] + static_cast<int64_t>(head) * D + part * 32, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -109,7 +137,8 @@ __global__ void __launch_bounds__(256, 5) kv4_append_kernel(const __grid_constan
   if (a.group >= 64) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   if (a.group >= 128) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
   if (slot < 0 || slot >= a.num_slots) return;
-  const __half s16 = __float2half_rn(fminf(__fdiv_rn(__fmul_rn(m, norm), 7.0f), 65504.f));
+  const float s32 = __fdiv_rn(__fmul_rn(m, norm), 7.0f);
+  const __half s16 = __float2half_rn(s32 > 65504.f ? 65504.f : s32);      // a NaN stays one
   const float s = __half2float(s16);
   const float f = s > 0.f ? __fdiv_rn(norm, s) : 0.f;
   const uint32_t page = a.page_size(static_cast<uint32_t>(slot));
@@ -160,7 +189,7 @@ __global__ void __launch_bounds__(256, 5) kv4_append_kernel(const __grid_constan
 // form of K's products took 60.5 us, one tile a step 73, V's 8 taken off by
 // products of its own 65, 24 warps instead of 16 (fewer registers) 64.
 //
-// Rounding: q to 2^-15 of its tile's largest value (digits) or to fp16, P to
+// Rounding: q to 2^-15 of its row's largest value (digits) or to fp16, P to
 // fp16 (2^-11 relative; the running maximum bounds it by 2^8).  Codes are exact,
 // scales multiply in fp32, and sums, maxima and the output accumulate in fp32.
 //
@@ -193,6 +222,7 @@ struct AttnArgs {
 };
 
 constexpr int kWarps = 4;
+constexpr float kLowest = -3.0e38f;           // no maximum yet: finite, so that its differences are numbers
 
 // A step is two tiles: 32 positions whose products, maximum and exponentials
 // interleave.
@@ -208,9 +238,9 @@ struct Cfg {
   static constexpr int JOIN_BYTES = kWarps * ROWS * (JOIN_STRIDE + 2) * 4;
   static constexpr int MAIN_BYTES = kWarps * RING_BYTES;
   static constexpr int BUF_BYTES = MAIN_BYTES > JOIN_BYTES ? MAIN_BYTES : JOIN_BYTES;
-  static constexpr int Q_AT = BUF_BYTES;                    // query rows as operands, and the warps' maxima
+  static constexpr int Q_AT = BUF_BYTES;                    // query rows as operands, and their units
   static constexpr int Q_BYTES = ROWS * D * 2;
-  static constexpr int VALID_AT = Q_AT + Q_BYTES + 16;      // valid positions of the tiles in flight
+  static constexpr int VALID_AT = Q_AT + Q_BYTES + ROWS * 4;   // valid positions of the tiles in flight
   static constexpr int SMEM_BYTES = VALID_AT + kWarps * STAGES * 8;
 };
 
@@ -384,7 +414,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     qraw[ps] = make_uint4(0u, 0u, 0u, 0u);
     if (row < C::ROWS && rho < rows) {
       const int i = static_cast<int>(a.ratio(rho)), head = h * ratio + rho - i * ratio;
-      qraw[ps] = ldg_stream(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride +
+      qraw[ps] = ld_stream(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.q_len + i) * a.q_stride +
                                                            static_cast<int64_t>(head) * D + 8 * (threadIdx.x % LPR)));
     }
   }
@@ -394,7 +424,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   const int steps = (len + 31) >> 5, per = (steps + a.splits - 1) / a.splits;
   const int t0 = min(split * per, steps), count = min(per, steps - t0);
   if (a.splits > 1 && count == 0) {             // nothing here: no part (the join skips sums of 0)
-    if (threadIdx.x < C::ROWS) a.part_ml[part + threadIdx.x] = make_float2(-1.0e30f, 0.f);
+    if (threadIdx.x < C::ROWS) a.part_ml[part + threadIdx.x] = make_float2(kLowest, 0.f);
     return;
   }
   const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;   // steps, interleaved over the warps
@@ -461,7 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
   // (every word in a group of its own).  D / 8 lanes rotate a row, 8 elements
   // each, and leave it in the order in which lane (r, c) takes row r.
   uint4* qs = reinterpret_cast<uint4*>(smem + C::Q_AT);       // [row / 8][word][lane]
-  float* tops = reinterpret_cast<float*>(smem + C::Q_AT + C::Q_BYTES);
+  float* row_unit = reinterpret_cast<float*>(smem + C::Q_AT + C::Q_BYTES);
   float v[PASSES][8], f = a.scale_log2;
   if (a.rotate) f *= a.norm;
 #pragma unroll
@@ -484,23 +514,20 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[ps][i] *= f;
   }
-  float mx = 0.f;
-#pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) mx = fmaxf(mx, absmax_regs(v[ps], 0, 8));
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if (lane == 0) tops[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, tops[w]);
-  const int eb = min(max(static_cast<int>(__float_as_uint(mx) >> 23), 16), 220);
-  const float ulp = __uint_as_float(static_cast<uint32_t>(eb) << 23);        // 2^e <= the tile's largest < 2^(e + 1)
-  const float down = __uint_as_float(static_cast<uint32_t>(254 - eb) << 23);
-  const float kf = G == 1 ? ulp * (1.f / 262144.f) : ulp * 16777216.f;
 #pragma unroll
   for (int ps = 0; ps < PASSES; ++ps) {
     const int row = ps * PASS + threadIdx.x / LPR, part8 = threadIdx.x % LPR;
     const int w = G == 1 ? part8 % NG : part8 / 4, qc = G == 1 ? part8 / NG : part8 % 4;
+    // a row of its own size: 2^e <= its largest value < 2^(e + 1).  Magnitudes
+    // compare as integers, and so do infinities and NaNs, which max would drop.
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(v[ps][i]) & 0x7fffffffu);
+#pragma unroll
+    for (int s = 1; s < LPR; s <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const int eb = min(max(static_cast<int>(mx >> 23), 16), 220);
+    const float up = __uint_as_float(static_cast<uint32_t>(eb) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(254 - eb) << 23);
     uint4 x;
     if constexpr (G == 1) {
       // digits of round(q 2^14 / 2^e) = 256 high + low: even elements' high
@@ -520,13 +547,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
       x.z = pack_half2(v[ps][2] * down, v[ps][6] * down);
       x.w = pack_half2(v[ps][3] * (down * 0.0625f), v[ps][7] * (down * 0.0625f));
     }
-    if (row < C::ROWS) qs[((row >> 3) * NG + w) * 32 + (row & 7) * 4 + qc] = x;
+    if (row < C::ROWS) {
+      qs[((row >> 3) * NG + w) * 32 + (row & 7) * 4 + qc] = x;
+      // of its products' sums; no number for a row that is none, or beyond 2^94
+      if (part8 == 0) row_unit[row] = (mx >> 23) > 220u ? __uint_as_float(0x7fc00000u) : up * (G == 1 ? 1.f / 262144.f : 16777216.f);
+    }
   }
   __syncthreads();
   uint4 qb[NT == 1 ? NG : 1];                 // one tile of rows: in registers; two: read at each use
   auto query = [&](int nt, int w) { return NT == 1 ? qb[w] : qs[(nt * NG + w) * 32 + lane]; };
   float bias[NT][G][2];                       // G > 1: what the 8 in (code + 8) adds to a row's sums, negative
-  int limit[NT][2];                           // first position that rows 2c, 2c + 1 do not see
+  float qf[NT][2];                            // units of the sums of rows 2c, 2c + 1
+  int limit[NT][2];                           // first position that they do not see
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -548,6 +580,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     for (int e = 0; e < 2; ++e) {
       const int col = rt * C::ROWS + nt * 8 + 2 * c + e;
       limit[nt][e] = len - a.q_len + 1 + static_cast<int>(a.ratio(col));
+      qf[nt][e] = row_unit[nt * 8 + 2 * c + e];
     }
   }
 
@@ -563,7 +596,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m[nt][e] = -1.0e30f, l[nt][e] = 0.f, ones[nt][e] = ones[nt][2 + e] = 0.f;
+    for (int e = 0; e < 2; ++e) m[nt][e] = kLowest, l[nt][e] = 0.f, ones[nt][e] = ones[nt][2 + e] = 0.f;
 
   // positions below this are seen by every row of the tile
   const int seen_by_all = len - a.q_len + 1 + static_cast<int>(a.ratio(rt * C::ROWS));
@@ -681,17 +714,25 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
         float k2[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          k2[e] = __half2float(kst[tt * 16 * G + 8 * e * G + g]) * kf;
+          k2[e] = __half2float(kst[tt * 16 * G + 8 * e * G + g]);
           kk[tt][e] = G == 1 ? k2[e] : 1.f;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            s[tt][nt][k] = G == 1 ? acc[tt][nt][k]
+            s[tt][nt][k] = G == 1 ? acc[tt][nt][k] * qf[nt][k & 1]
                            : g == 0 ? acc[tt][nt][k] * k2[k >> 1]
                                     : fmaf(acc[tt][nt][k], k2[k >> 1], s[tt][nt][k]);
       }
+    }
+    if constexpr (G > 1) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[tt][nt][k] *= qf[nt][k & 1];
     }
     // V's scales of this lane's four positions, and log2 of the largest of each
     float sv[2][2][G], lv[2][2];
@@ -702,8 +743,16 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 #pragma unroll
         for (int g = 0; g < G; ++g) sv[tt][e][g] = __half2float(vst[tt * 16 * G + 8 * e * G + g]);
     const bool masked = nv.x + nv.y < 32 || pos + 32 > seen_by_all;
+    float none[2][2] = {};
     if (masked) {
-      // finite scales, so that a position that a row does not see adds 0 whatever lies there
+      // finite scales, so that a position that a row does not see adds 0 whatever
+      // lies there; the score of a row that does see it takes the NaN
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < G; ++g) none[tt][e] = fmaf(sv[tt][e][g], 0.f, none[tt][e]);
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
@@ -718,7 +767,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
         float top = fabsf(sv[tt][e][0]);
 #pragma unroll
         for (int g = 1; g < G; ++g) top = fmaxf(top, fabsf(sv[tt][e][g]));
-        lv[tt][e] = fmaxf(log2_fast(top), -24.f);          // the least fp16 above zero is 2^-24
+        lv[tt][e] = fminf(fmaxf(log2_fast(top), -24.f), 16.f);   // fp16 above zero: 2^-24 to 2^16
       }
     if (masked) {
 #pragma unroll
@@ -729,7 +778,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
           const bool there = at < (tt ? nv.y : nv.x);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            s[tt][nt][k] = there && pos + 16 * tt + at < limit[nt][k & 1] ? s[tt][nt][k] * kk[tt][k >> 1] : -INFINITY;
+            s[tt][nt][k] = there && pos + 16 * tt + at < limit[nt][k & 1] ? fmaf(s[tt][nt][k], kk[tt][k >> 1], none[tt][k >> 1])
+                                                                                : -INFINITY;
         }
         kk[tt][0] = kk[tt][1] = 1.f;
       }
@@ -755,7 +805,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-          t = fmaxf(t, m[nt][e]);
+          t = t > m[nt][e] + 8.f ? t : m[nt][e];     // no row depends on its neighbours' sizes
           const float f = exp2_fast(m[nt][e] - t);
           m[nt][e] = t;
           l[nt][e] *= f;
@@ -881,7 +931,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     const int rho = rt * C::ROWS + row;
     if (rho >= rows) continue;
     float2 ml[kWarps];
-    float top = -1.0e30f, sum = 0.f;
+    float top = kLowest, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -898,7 +948,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
     if (a.splits == 1) {
       const int qi = static_cast<int>(a.ratio(rho));
       const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads.d * ratio) + h * ratio + rho - qi * ratio;
-      const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;      // a row that sees nothing: zeros
+      const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);     // a row that sees nothing: zeros
       *reinterpret_cast<uint2*>(a.out + orow * D + d) = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
     } else {
       *reinterpret_cast<float4*>(a.part_o + (part + row) * D + d) = y;
@@ -927,7 +977,7 @@ __global__ void __launch_bounds__(32 * ROWS * kPieces<ROWS>, 1) kv4_join_kernel(
   const bool live = rho < a.q_len * ratio;
   const int s0 = a.splits * piece / pieces, s1 = live ? a.splits * (piece + 1) / pieces : s0;
   auto part_row = [&](int s) { return (static_cast<int64_t>(s) * a.units + unit) * ROWS + row; };
-  float top = -1.0e30f;
+  float top = kLowest;
   for (int s = s0 + lane; s < s1; s += 32) top = fmaxf(top, a.part_ml[part_row(s)].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -950,14 +1000,14 @@ __global__ void __launch_bounds__(32 * ROWS * kPieces<ROWS>, 1) kv4_join_kernel(
     }
     sum = fmaf(ml.y, f, sum);
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = ml.y > 0.f ? fmaf(y[i], f, v[i]) : v[i];   // an empty part was not written
+    for (int i = 0; i < E; ++i) v[i] = ml.y == 0.f ? v[i] : fmaf(y[i], f, v[i]);   // an empty part was not written
   }
 #pragma unroll
   for (int i = 0; i < E; ++i) part[piece][row][lane * E + i] = v[i];
   if (lane == 0) part_ml[piece][row] = make_float2(top, sum);
   __syncthreads();
   if (piece != 0 || !live) return;
-  float all = -1.0e30f;
+  float all = kLowest;
   for (int i = 0; i < pieces; ++i) all = fmaxf(all, part_ml[i][row].x);
   sum = 0.f;
 #pragma unroll
@@ -969,7 +1019,7 @@ __global__ void __launch_bounds__(32 * ROWS * kPieces<ROWS>, 1) kv4_join_kernel(
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = fmaf(part[q][row][lane * E + i], f, v[i]);
   }
-  const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+  const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
   const int64_t orow = (static_cast<int64_t>(b) * a.q_len + qi) * (a.kv_heads.d * ratio) + h * ratio + rho - qi * ratio;
 #pragma unroll
   for (int i = 0; i < E; i += 2)

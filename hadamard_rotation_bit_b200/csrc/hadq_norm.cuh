@@ -26,25 +26,22 @@
 namespace hadq {
 namespace norm {
 
-// 8 consecutive elements; x may be the buffer that the kernel also writes, so
-// no read-only-cache load.
+// 8 consecutive elements (x may be the buffer that the kernel also writes).
 template <bool BF16>
 __device__ __forceinline__ void load8(const void* p, int64_t e, float (&v)[8]) {
   if constexpr (BF16) {
-    uint4 w;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                 : "l"(static_cast<const uint16_t*>(p) + e));
+    const uint4 w = ld_stream(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e));
     unpack_bf16x2(w.x, v[0], v[1]);
     unpack_bf16x2(w.y, v[2], v[3]);
     unpack_bf16x2(w.z, v[4], v[5]);
     unpack_bf16x2(w.w, v[6], v[7]);
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
-                   : "l"(static_cast<const float*>(p) + e + 4 * h));
+    for (int h = 0; h < 2; ++h) {
+      const uint4 w = ld_stream(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + e + 4 * h));
+      v[4 * h] = __uint_as_float(w.x), v[4 * h + 1] = __uint_as_float(w.y);
+      v[4 * h + 2] = __uint_as_float(w.z), v[4 * h + 3] = __uint_as_float(w.w);
+    }
   }
 }
 
@@ -160,7 +157,7 @@ __device__ __forceinline__ void add8(float (&t)[8], const float (&r)[8]) {
 // CTAs of T threads times RPC rows; T = 32 takes a warp per row (no barrier).
 template <bool BF16, bool RES, int T, int RPC, int NV>
 __global__ void __launch_bounds__(T * RPC)
-rmsnorm_quant_kernel(const void* x, const void* res, const void* __restrict__ weight, int64_t rows, int n, float eps,
+rmsnorm_quant_kernel(const void* x, const void* res, const void* weight, int64_t rows, int n, float eps,
                      void* stream_out, int8_t* __restrict__ codes, float* __restrict__ scales) {
   static_assert(T == 32 || RPC == 1, "rows of several warps have a CTA of their own");
   grid_dependency_sync();
@@ -225,7 +222,7 @@ rmsnorm_quant_kernel(const void* x, const void* res, const void* __restrict__ we
   }
   if (tid == 0) {
     const float rms = __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(n)) + eps);
-    scales[row] = __fdiv_rn(__fdiv_rn(m, rms), 127.0f);
+    scales[row] = m == 0.f && ss == 0.f ? 0.f : __fdiv_rn(__fdiv_rn(m, rms), 127.0f);   // eps may be 0
   }
 }
 
@@ -256,7 +253,7 @@ constexpr int kMaxStages = 8;
 // `stages` rows of x (and of the residual) in flight per CTA.
 template <bool BF16, bool RES, int T, int NV>
 __global__ void __launch_bounds__(T)
-rmsnorm_ring_kernel(const void* x, const void* res, const void* __restrict__ weight, int64_t rows, int n, float eps,
+rmsnorm_ring_kernel(const void* x, const void* res, const void* weight, int64_t rows, int n, float eps,
                     void* stream_out, int8_t* __restrict__ codes, float* __restrict__ scales, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
@@ -342,7 +339,7 @@ rmsnorm_ring_kernel(const void* x, const void* res, const void* __restrict__ wei
     }
     if (tid == 0) {
       const float rms = __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(n)) + eps);
-      scales[row] = __fdiv_rn(__fdiv_rn(m, rms), 127.0f);
+      scales[row] = m == 0.f && ss == 0.f ? 0.f : __fdiv_rn(__fdiv_rn(m, rms), 127.0f);   // eps may be 0
     }
   }
 }

@@ -272,7 +272,7 @@ HADQ_API hadq_status hadq_rotate_quant_codebook(const void* x, hadq_dtype x_dtyp
  *     h = x + residual            (rounded to x_dtype; h = x without residual)
  *     t = h * weight              (fp32 product)
  *     q = rne(127 t / max|t|)     in [-127, 127]; all 0 when max|t| = 0
- *     s = max|t| / (127 sqrt(mean(h^2) + eps))
+ *     s = max|t| / (127 sqrt(mean(h^2) + eps))    0 when max|t| = 0
  * so that q * s is RMSNorm(h) * weight.  The codes are exact: the norm's
  * factor cancels in them, and the quotient's rounding is that of the reals.
  * The sum of squares is held in fp32.
@@ -322,7 +322,8 @@ HADQ_API hadq_status hadq_matmul_int8(const int8_t* a, const float* a_scales, in
  * unnormalised sums and c = fp32(1/sqrt(head_dim)) (1 unrotated),
  *     s = fp16(min(fp32(fp32(M c) / 7), 65504)),  q = clamp(rne(z * fp32(c / s)), -7, 7),
  * s = 0 giving codes 0: HADQ_INT4_SYM, except that a scale beyond fp16
- * saturates instead of becoming infinite.
+ * saturates instead of becoming infinite.  The absmax passes over NaNs unless
+ * the whole group is NaN (a rotated row with one NaN is), whose scale is NaN.
  *   k, v       row (t, h) at k + t * k_stride + h * head_dim, in elements of
  *              dtype: slices of a fused projection's output need no copy.
  *              k_stride, v_stride: at least kv_heads * head_dim, a multiple of
@@ -360,11 +361,14 @@ HADQ_API hadq_status hadq_kv4_append(const void* k, int64_t k_stride, const void
  *              of device memory (null when that is 0), written and read by
  *              this call: calls that may run at the same time need one each
  * Positions beyond a length are never read as numbers: any bits may lie there.
+ * A query row that holds an infinity or a NaN, or that reaches 2^94 once it is
+ * rotated and multiplied by scale log2(e), gives NaN, as does one that sees a
+ * scale that is no number; other rows are what they are without it.
  * The codes enter the products exactly.  q R is rounded for them: with one
- * scale per row (group = head_dim) to 16 bits below the largest value of its
- * tile of 8 or 16 query rows (2^-15 of it, summed exactly in integers), with
- * more to fp16 (2^-11 of each value); probabilities to fp16 (2^-11).  Maxima,
- * sums and the output are held in fp32.  Results do not depend on the order of
+ * scale per cached row (group = head_dim) to 2^-15 of its own row's largest
+ * value (the products are then summed exactly, in integers), with more to fp16
+ * (2^-11 of each value); probabilities to fp16 (2^-11).  Maxima, sums and the
+ * output are held in fp32.  Results do not depend on the order of
  * execution.
  */
 HADQ_API hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype, int64_t batch,

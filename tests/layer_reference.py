@@ -19,7 +19,7 @@ def norm(x, weight, eps, residual=None):
     t = (h.float() * weight.float()).double()
     top = t.abs().amax(-1, keepdim=True)
     codes = torch.where(top > 0, torch.round(127.0 * t / torch.where(top > 0, top, 1.0)), 0.0).to(torch.int8)
-    scales = top[..., 0] / (127.0 * torch.sqrt((h.double() ** 2).mean(-1) + eps))
+    scales = torch.where(top[..., 0] > 0, top[..., 0] / (127.0 * torch.sqrt((h.double() ** 2).mean(-1) + eps)), 0.0)
     return codes, scales, stream
 
 
@@ -78,9 +78,8 @@ def cached_rows(codes, scales, pages, n):
 def attention(q, cache, table, lengths, scale, rotate):
     """(out, tolerance) in 64 bits: q [batch, q_len, heads, d].
 
-    The bound: the rotated q is rounded to 2^-15 of the largest value of its
-    tile's rows (taken over all rows that share the K/V head) where a row has
-    one scale, so a score is off by at most scale 2^-15 max|q| sum |k_d|; with
+    The bound: the rotated q is rounded to 2^-15 of its row's largest value
+    where a cached row has one scale, so a score is off by at most scale 2^-15 max|q| sum |k_d|; with
     more scales to fp16, off by 2^-11 per value, scale 2^-11 sum |q_d k_d|.
     The fp32 rotation and sums of at most 128 products add less than 2^-16 of
     sum |q_d k_d|, taken as 2^-15 of it.  With e the whole, p is off by a factor
@@ -88,6 +87,11 @@ def attention(q, cache, table, lengths, scale, rotate):
     or, below 2^-14, by at most 2^-25 per position against codes of at most 8
     in units of the scale of the position that leads the running maximum; exp2
     and the fp32 sums take another 2^-14; the result is rounded to bf16.
+    Where e is so large that exp(2 e) says nothing (it is infinite from e = 355
+    on), a second bound holds as well: whatever the p are, both results are
+    means of the same values with weights that sum to 1, so they lie between
+    the smallest and the largest of them and differ by at most their distance,
+    next to the roundings above, which are relative to the values.
     """
     k_codes, k_scales, v_codes, v_scales = cache
     page = k_codes.shape[2]
@@ -106,7 +110,6 @@ def attention(q, cache, table, lengths, scale, rotate):
         k = cached_rows(k_codes, k_scales, pages, n).repeat_interleave(ratio, 0)      # [heads, n, d]
         v = cached_rows(v_codes, v_scales, pages, n).repeat_interleave(ratio, 0)
         rows = q[b].double() @ rot if rotate else q[b].double()                      # [q_len, heads, d]
-        largest = rows.abs().amax((0, 2)).view(kv_heads, ratio).amax(1).repeat_interleave(ratio)
         sv = v_scales[pages].transpose(0, 1).flatten(1, 2)[:, :n].double().abs().amax((1, 2)).repeat_interleave(ratio, 0)
         for i in range(q_len):
             m = n - q_len + i + 1
@@ -117,13 +120,18 @@ def attention(q, cache, table, lengths, scale, rotate):
             y = torch.einsum("hm,hmd->hd", p, v[:, :m])
             products = torch.einsum("hd,hmd->hm", row.abs(), k[:, :m].abs())
             if one_scale:
-                e = 2.0 ** -15 * (products + largest[:, None] * k[:, :m].abs().sum(-1))
+                e = 2.0 ** -15 * (products + row.abs().amax(1, keepdim=True) * k[:, :m].abs().sum(-1))
             else:
                 e = (2.0 ** -15 + 2.0 ** -11) * products
             e = abs(scale) * e.amax(-1)
             spread = torch.einsum("hm,hmd->hd", p, v[:, :m].abs())
             out[b, i] = y
-            tol[b, i] = (y.abs() * HALF[torch.bfloat16]
-                         + spread * (torch.expm1(2 * e)[:, None] + 2.0 ** -11 + 2.0 ** -14) * (1 + HALF[torch.bfloat16])
-                         + (m * 2.0 ** -22 * sv)[:, None])
+            rounding = (2.0 ** -11 + 2.0 ** -14) * (1 + HALF[torch.bfloat16])
+            factor = (1 + HALF[torch.bfloat16]) * torch.expm1(2 * e)[:, None]
+            near = (y.abs() * HALF[torch.bfloat16] + spread * rounding
+                    + torch.where(spread > 0, spread * factor, 0.0) + (m * 2.0 ** -22 * sv)[:, None])
+            low, high = v[:, :m].amin(1), v[:, :m].amax(1)
+            hull = (high - low) + torch.maximum(low.abs(), high.abs()) * (HALF[torch.bfloat16] + rounding) \
+                + (m * 2.0 ** -22 * sv)[:, None]
+            tol[b, i] = torch.where(torch.isinf(factor), hull, near)
     return out, tol

@@ -122,6 +122,28 @@ def test_norm_in_place(rows, n, target):
     assert torch.equal(r if target == "x" else x, r0 if target == "x" else x0)
 
 
+@pytest.mark.parametrize("rows,n", [(3, 256), (5000, 4096)])
+def test_norm_zero_rows_without_eps(rows, n):
+    x, w = torch.zeros((rows, n), device="cuda"), torch.ones(n, device="cuda")
+    x[1] = 1.0
+    codes, scales, _ = H.hadq_rmsnorm_quant(x, w, 0.0)
+    check_norm(x, w, 0.0, None, codes, scales, None)
+    assert float(scales[0]) == 0.0 and int(codes[1, 5]) == 127
+
+
+@pytest.mark.parametrize("rows,n", [(3, 256), (5000, 4096)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_norm_shows_rows_that_are_no_numbers(rows, n, bad):
+    x, w = randn(gen(5), rows, n), torch.ones(n, device="cuda")
+    codes, scales, _ = H.hadq_rmsnorm_quant(x, w, 1e-6)
+    x[1, 7] = bad
+    x[2] = math.nan
+    codes_, scales_, _ = H.hadq_rmsnorm_quant(x, w, 1e-6)
+    assert bool(scales_[1:3].isnan().all())
+    keep = [i for i in range(rows) if i not in (1, 2)]
+    assert torch.equal(codes[keep], codes_[keep]) and torch.equal(scales[keep], scales_[keep])
+
+
 def test_norm_leading_dimensions_and_empty():
     g = gen(6)
     x, w = randn(g, 2, 3, 128), randn(g, 128)
@@ -282,6 +304,15 @@ def test_append_huge_rows_saturate(size, saturates):
     assert (float(cache[3].float().max()) == 65504.0) == saturates
 
 
+def test_append_shows_rows_that_are_no_numbers():
+    k = randn(gen(24), 3, 2, 128)
+    k[1, 0, 9] = math.nan
+    cache = new_cache(gen(25), 1, 2, 16, 128, 32)
+    H.hadq_kv4_append(k, k, torch.arange(3, device="cuda"), *cache)
+    assert bool(cache[1][0, 0, 1].isnan().all()) and int(cache[1][0, :, :3].isnan().sum()) == 4
+    assert not bool(cache[3].isnan().any())
+
+
 def test_append_slots_outside_the_cache_are_recorded():
     g = gen(23)
     k = randn(g, 5, 2, 64, dtype=torch.bfloat16)
@@ -350,6 +381,51 @@ def test_attention_large_and_tiny_queries():
     q = (q.float() * size).to(torch.bfloat16)
     out = H.hadq_kv4_attention(q, *cache, table, ln, scale=1e-3)
     check_attention(out, q, cache, table, ln, 1e-3, True)
+
+
+@pytest.mark.parametrize("group", [128, 32])
+def test_attention_rows_of_one_tile_do_not_disturb_each_other(group):
+    """Heads that share a K/V head, 2^40 apart in size, one of them infinite: every other row is what it is alone."""
+    q, cache, table, ln = attention_case(14, 1, 2, 2, 4, 128, group, 16, [45])
+    size = torch.tensor([1.0, 2.0 ** 20, 2.0 ** -20, 1.0, 1.0, 1.0, 3.0, 1.0], device="cuda").view(1, 1, 8, 1)
+    q = (q.float() * size).to(torch.bfloat16)
+    out = H.hadq_kv4_attention(q, *cache, table, ln, scale=0.05)
+    check_attention(out, q, cache, table, ln, 0.05, True)
+    bad = q.clone()
+    bad[0, 0, 3], bad[0, 1, 5, 7] = math.inf, math.nan
+    got = H.hadq_kv4_attention(bad, *cache, table, ln, scale=0.05)
+    keep = torch.ones((1, 2, 8), dtype=torch.bool, device="cuda")
+    keep[0, 0, 3] = keep[0, 1, 5] = False
+    assert torch.equal(got[keep], out[keep])
+    assert bool(got[~keep].isnan().all())
+
+
+@pytest.mark.parametrize("d,group,n", [(128, 128, 45), (128, 32, 45), (64, 64, 2100), (128, 128, 9000)])
+@pytest.mark.parametrize("which", [1, 3])
+def test_attention_shows_scales_that_are_no_numbers(d, group, n, which):
+    """A NaN or an infinity as the scale of a position: the K/V head's rows that see it are no numbers, the others are untouched."""
+    q, cache, table, ln = attention_case(15, 2, 2, 2, 2, d, group, 16, [n, n])
+    want = H.hadq_kv4_attention(q, *cache, table, ln)
+    for value, at in ((math.nan, 0), (math.inf, 0), (math.nan, n - 1), (math.inf, n - 1), (math.nan, n // 2)):
+        dirty = [t.clone() for t in cache]
+        dirty[which][table[1, at // 16].long(), 1, at % 16] = value
+        got = H.hadq_kv4_attention(q, *dirty, table, ln)
+        first = 1 if at == n - 1 else 0                # the newest position is seen by the last query alone
+        keep = torch.ones_like(got, dtype=torch.bool)
+        keep[1, first:, 2:] = False
+        assert torch.equal(got[keep], want[keep])
+        if which == 3 or math.isnan(value):            # K: an infinite score of -inf is a position without weight
+            assert not bool(got[1, first:, 2:].isfinite().any())
+
+
+def test_attention_far_scores():
+    """Scores down to -2^100: the least of them still sum to one."""
+    q, cache, table, ln = attention_case(16, 1, 1, 1, 2, 128, 128, 16, [3])
+    cache[0].fill_(0x11), cache[1].fill_(60000.0)
+    q = torch.full_like(q, -(2.0 ** 86))
+    out = H.hadq_kv4_attention(q, *cache, table, ln, block=1, scale=0.25)
+    v = R.cached_rows(cache[2], cache[3], table[0].long(), 3)
+    assert bool((out[0, 0].double() - v.mean(1)).abs().le(v.abs().mean(1) * 2.0 ** -7).all())
 
 
 @pytest.mark.parametrize("bits", [0x7C00, 0xFC00, 0x7E00, 0xFBFF])
