@@ -354,6 +354,7 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(C::TMEM_COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
   }
+  if (splits > 1) cluster_arrive();           // waited for before the first access to another CTA's memory
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -154,3 +154,18 @@ def test_token_spacing(shape, stride, want):
 def test_token_spacing_refusals(shape, stride):
     with pytest.raises(H.HadqError):
         H._token_rows("x", torch.zeros(8000).as_strided(shape, stride), shape[-2:])
+
+
+def test_every_cluster_barrier_is_arrived_at_before_it_is_waited_for():
+    """Read from the source: a wait without its arrival returns early, which no result has to show."""
+    import re
+    from pathlib import Path
+
+    text = (Path(hbuild.__file__).parent / "csrc" / "hadq_imm.cuh").read_text()
+    kernels = re.split(r"^imm_\w+_kernel\(", text, flags=re.M)[1:]
+    seen = 0
+    for body in kernels:
+        calls = re.findall(r"cluster_(arrive|wait)\(\);", body)
+        assert calls == ["arrive", "wait"] * (len(calls) // 2)
+        seen += len(calls)
+    assert seen >= 8
