@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) imm_warp_kernel(const __gri
         y[t][e] = in ? ld_stream(reinterpret_cast<const uint4*>(w[t][e] + 64 * i)) : make_uint4(0u, 0u, 0u, 0u);
   };
   auto step = [&](int i, uint4 (&y)[MT][2]) {
-    const int at = 64 * i + 16 * c < p.k ? 64 * i : 0;   // any bytes will do against zeros
+    const int at = 64 * i + 16 * c < p.k ? 64 * i : -16 * c;   // any bytes of the row will do against zeros
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const uint4 b = *reinterpret_cast<const uint4*>(a[u] + at);

@@ -185,6 +185,21 @@ def test_matmul(m, n, k, out):
     check()
 
 
+@pytest.mark.parametrize("k", [16, 32, 48, 80])
+@pytest.mark.parametrize("m", [5, 8, 11, 16])
+def test_matmul_rows_shorter_than_a_round(m, k):
+    """The bytes beside the last row hold no part of the result: the same in a buffer of its own and between others."""
+    g = gen(m + k)
+    wide = torch.randint(-127, 128, (m + 2, k), generator=g, device="cuda", dtype=torch.int8)
+    a, w = wide[1:-1], torch.randint(-127, 128, (33, k), generator=g, device="cuda", dtype=torch.int8)
+    sa, sw = torch.rand(m, generator=g, device="cuda"), torch.rand(33, generator=g, device="cuda")
+    out = H.hadq_matmul_int8(a, sa, w, sw, out_dtype=torch.float32)
+    check_matmul(out, a, sa, w, sw, None)
+    wide[0], wide[-1] = 127, -128
+    assert torch.equal(out, H.hadq_matmul_int8(a.clone(), sa, w, sw, out_dtype=torch.float32))
+    assert torch.equal(out, H.hadq_matmul_int8(a, sa, w, sw, out_dtype=torch.float32))
+
+
 @pytest.mark.parametrize("m,n", [(1, 130), (3, 33), (9, 40), (17, 65), (200, 300)])
 def test_matmul_largest_sums(m, n):
     """-128 x -128 over the longest k: 2147221504, just inside 32 bits."""
