@@ -627,7 +627,8 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention of each sequence's newest tokens q [batch, q_len, heads, head_dim]
     (or [batch, heads, head_dim]) over the paged int4 cache (see include/hadq.h).
-    scale: 1 / sqrt(head_dim) when None.  Without ``workspace`` one is allocated."""
+    scale: 1 / sqrt(head_dim) when None.  Without ``workspace`` one is allocated, of
+    ``stream``."""
     lib = _lib or load_library()
     dev, dtype, shape = q.get_device(), q.dtype, q.shape
     ptrs, pages, kv_heads, size, d, group = _kv4_cache(dev, k_codes, k_scales, v_codes, v_scales)
@@ -648,8 +649,11 @@ def hadq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.T
     nbytes, ws = 0, None
     if workspace is None:
         need = _kv4_workspace(batch, q_len, heads, kv_heads, d, max_pages * size)
-        if need > 0:
+        if need > 0 and stream is None:
             workspace = q.new_empty(need, dtype=torch.uint8)
+        elif need > 0:                         # of the stream that uses it: nobody else holds it until then
+            with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), dev)):
+                workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None:
         _takes("workspace", workspace, dev, workspace.dtype, workspace.shape)
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

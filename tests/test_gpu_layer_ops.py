@@ -480,6 +480,26 @@ def test_attention_bad_pages_and_lengths_are_recorded():
     assert not bool(out[0].any()) and torch.equal(out[2], want[2])
 
 
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_attention_on_another_stream_keeps_its_workspace(as_handle):
+    """Memory that this stream asks for after the call is not what the other stream still computes in."""
+    q, cache, table, ln = attention_case(17, 1, 1, 2, 4, 128, 128, 16, [4000])
+    need = H.hadq_kv4_attention_workspace(1, 1, 8, 2, 128, table.shape[1] * 16)
+    assert need > 0
+    want, out = H.hadq_kv4_attention(q, *cache, table, ln), torch.empty_like(q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)                 # about a millisecond
+        H.hadq_kv4_attention(q, *cache, table, ln, out=out, stream=side.cuda_stream if as_handle else side)
+        noise = [torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del noise
+    assert torch.equal(H.hadq_kv4_attention(q, *cache, table, ln, stream=0 if as_handle else torch.cuda.default_stream()), want)
+
+
 def test_attention_query_slices_and_three_dimensions():
     g = gen(11)
     _, cache, table, ln = attention_case(11, 3, 1, 2, 4, 128, 128, 16, [20, 0, 45])
