@@ -16,18 +16,22 @@
 //       operands no longer fit beside the loads.
 //   imm_warp_kernel   up to 16 tokens: the same, with the warps' matrix
 //       instructions.  8 and 16 tokens, 4096 x 4096: 4.7 and 4.9 us against 6.5
-//       and 6.5 of the split kernel; 4096 x 14336: 13.0 and 13.1 against 13.7
-//       and 13.7.  From 32 tokens on the token loads of every warp cost more
+//       and 6.5 of the split kernel; 4096 x 14336: 13.0 and 13.1 against 13.4
+//       and 13.4.  From 32 tokens on the token loads of every warp cost more
 //       (8.4 against 7.4).
-//   imm_split_kernel  up to a few hundred tokens: bound by reading w.  Output channels are the
-//       MMA's 128 rows and TN tokens its columns, so one token costs no more
-//       traffic than it has, and the CTAs of a cluster share the k of a tile,
-//       adding their sums through distributed shared memory.
+//   imm_split_kernel  up to a few hundred tokens: bound by reading w.  Output
+//       channels are the MMA's 128 rows and TN tokens its columns, so one token
+//       costs no more traffic than it has, and the CTAs of a cluster share the k
+//       of a tile, adding their sums through distributed shared memory.  48 x
+//       14336 x 4096: 13.6 us, of which the loads alone take 9 and launch, start
+//       and epilogue the rest; tiles of 96 to 120 channels, so that every SM has
+//       one, take as long (13.5): memory is what all of them wait for.
 //   imm_pair_kernel   many tokens: bound by the tensor cores.  CTA pairs
 //       compute 256 x 256 tiles (cta_group::2), which halves the shared-memory
 //       and L2 reads per product of a single CTA's tile; persistent, two
 //       accumulators, so that the epilogue of a tile runs under the products
-//       of the next.
+//       of the next: eight warps, since with four it outlasted the products of
+//       k = 1024 (4096 x 4096: 24.7 us, with four 31.3).  8192 x 4096 x 14336: 305 us.
 //
 // The last two stage 128-byte slices of k by TMA (128-byte swizzle; the tail of
 // k and rows beyond a matrix are filled with zeros) into a ring that one thread
@@ -56,6 +60,7 @@ struct Args {
   const float* bias;   // nullptr: none
   void* out;
   int m, n, k;         // tokens, channels
+  int tokens;          // of a CTA of the split kernel
 };
 
 constexpr int kSlice = 128;   // bytes of k per stage
@@ -314,10 +319,11 @@ struct SplitCfg {
   static constexpr int THREADS = 128;
   static constexpr int SM_RING = 0;
   static constexpr int SM_JOIN = STAGES * STAGE_BYTES;                // [source rank][quad of columns][channel][4]
-  static constexpr int SM_BARS = SM_JOIN + TN * 128 * 4;
+  static constexpr int SM_SA = SM_JOIN + TN * 128 * 4;                // the tokens' scales
+  static constexpr int SM_BARS = SM_SA + TN * 4;
   static constexpr int SM_SLOT = SM_BARS + 8 * (2 * STAGES + 1);
-  static constexpr int SM_SA = SM_SLOT + 16;                          // the tokens' scales
-  static constexpr int SMEM_BYTES = SM_SA + TN * 4 + 1024;
+  static constexpr int SMEM_BYTES = SM_SLOT + 16 + 1024;
+  static constexpr int CTAS = 228 * 1024 / (SMEM_BYTES + 1024);       // on an SM
 };
 
 // CTA (tile, rank): channels ch0 .. ch0 + 127, tokens t0 .. t0 + TN - 1, the
@@ -337,7 +343,7 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 
   const int rank = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = blockIdx.x / splits;
-  const int ch0 = (tile / token_tiles) * 128, t0 = (tile % token_tiles) * TN;
+  const int ch0 = (tile / token_tiles) * 128, t0 = (tile % token_tiles) * p.tokens;
   const int slices = (p.k + kSlice - 1) / kSlice;
   const int s0 = static_cast<int>(static_cast<int64_t>(slices) * rank / splits);
   const int iters = static_cast<int>(static_cast<int64_t>(slices) * (rank + 1) / splits) - s0;   // >= 1
@@ -386,7 +392,7 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         tc::drain_loads(full, STAGES, i);
         break;
       }
-      mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+      mbar_arrive_expect_tx(&full[s], C::W_BYTES + p.tokens * kSlice);   // whole boxes
       uint8_t* dst = smem + C::SM_RING + s * C::STAGE_BYTES;
       tc::tma_load_2d(dst, &map_w, (s0 + i) * kSlice, ch0, &full[s]);
       tc::tma_load_2d(dst + C::W_BYTES, &map_a, (s0 + i) * kSlice, t0, &full[s]);
@@ -423,20 +429,35 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   ok = __all_sync(0xffffffffu, ok);
   __syncthreads();                            // sa
   tc_fence_after();
-  auto put = [&](int col, int acc) {          // column of the tile, its sum
-    if (live && t0 + col < p.m)
-      store_one<OUT_BF16>(p.out, static_cast<int64_t>(t0 + col) * p.n + ch, finish(scaled(acc, sa[col]), sw, biased, bias));
+  const int cols = min(p.tokens, p.m - t0);   // of this tile
+  // N columns of the tile from their sums: all of them computed before the first
+  // is stored, so that their latencies overlap (one after the other, each behind
+  // its own condition, they took 105 clocks a column).
+  auto put = [&](int col, const auto& acc) {
+    constexpr int N = sizeof(acc) / sizeof(int);
+    float y[N];
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(sa + col + j);
+      y[j] = finish(scaled(acc[j], s.x), sw, biased, bias);
+      y[j + 1] = finish(scaled(acc[j + 1], s.y), sw, biased, bias);
+      y[j + 2] = finish(scaled(acc[j + 2], s.z), sw, biased, bias);
+      y[j + 3] = finish(scaled(acc[j + 3], s.w), sw, biased, bias);
+    }
+    int64_t e = static_cast<int64_t>(t0 + col) * p.n + ch;
+#pragma unroll
+    for (int j = 0; j < N; ++j, e += p.n)
+      if (live && col + j < cols) store_one<OUT_BF16>(p.out, e, y[j]);
   };
   const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   if (splits == 1) {
     if (ok) {
 #pragma unroll 1
-      for (int c = 0; c < TN; c += 16) {
+      for (int c = 0; c < cols; c += 16) {
         int v[16];
         tmem_ld16i(taddr + c, v);
         tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) put(c + j, v[j]);
+        put(c, v);
       }
     }
   } else {
@@ -447,7 +468,7 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     cluster_wait();
     const uint32_t join = smem_u32(smem + C::SM_JOIN);
 #pragma unroll 1
-    for (int c = 0; c < TN; c += 16) {
+    for (int c = 0; c < cols; c += 16) {
       int v[16];
       tmem_ld16i(taddr + c, v);
       tmem_wait_ld();
@@ -467,7 +488,7 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     cluster_wait();
     const int* got = reinterpret_cast<const int*>(smem + C::SM_JOIN);
 #pragma unroll 2
-    for (int col = 0; col < mine; col += 4) {
+    for (int col = 0; col < min(mine, cols - rank * mine); col += 4) {
       int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -475,10 +496,8 @@ imm_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           const int4 x = *reinterpret_cast<const int4*>(got + ((r << lg) + col) * 128 + threadIdx.x * 4);
           sum = make_int4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
         }
-      put(rank * mine + col, sum.x);
-      put(rank * mine + col + 1, sum.y);
-      put(rank * mine + col + 2, sum.z);
-      put(rank * mine + col + 3, sum.w);
+      const int v[4] = {sum.x, sum.y, sum.z, sum.w};
+      put(rank * mine + col, v);
     }
   }
   tc_fence_before();
@@ -496,12 +515,14 @@ struct PairCfg {
   static constexpr int TILE = 256;                                    // tokens and channels of a pair's tile
   static constexpr int OP_BYTES = 128 * kSlice;                       // one CTA's half of an operand
   static constexpr int STAGE_BYTES = 2 * OP_BYTES;
-  static constexpr int THREADS = 32 * 6;                              // producer, MMA, four epilogue warps
+  static constexpr int EPI_WARPS = 8;                                 // two for each quarter of the rows
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);                // producer, MMA, epilogue
   static constexpr int SM_RING = 0;
   static constexpr int SM_BARS = STAGES * STAGE_BYTES;
   static constexpr int SM_SLOT = SM_BARS + 8 * (2 * STAGES + 4);
   static constexpr int SM_TURN = SM_SLOT + 16;                        // per epilogue warp: 32 rows x 33 words
-  static constexpr int SMEM_BYTES = SM_TURN + 4 * 32 * 33 * 4 + 1024;
+  static constexpr int SMEM_BYTES = SM_TURN + EPI_WARPS * 32 * 33 * 4 + 1024;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
@@ -553,7 +574,7 @@ imm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);                                    // four epilogue warps of each CTA
+      mbar_init(&acc_empty[b], 2 * C::EPI_WARPS);                     // the epilogue warps of each CTA
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -630,7 +651,8 @@ imm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     }
   } else {
     // ---------------------------------------------------- epilogue, both CTAs
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, c0 = (warp - 2) / 4 * 128;          // rows, first column of the warp
+    const bool biased = p.bias != nullptr;
     uint32_t n = 0;
     float* turn = reinterpret_cast<float*>(smem + C::SM_TURN) + (warp - 2) * 32 * 33;
     const uint32_t release = map_rank(smem_u32(acc_empty), 0);
@@ -638,22 +660,31 @@ imm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       int im, in;
       tile_at(t, mt, nt, &im, &in);
       const uint32_t b = n & 1;
+      const int row0 = im * C::TILE + rank * 128 + quarter * 32, col0 = in * C::TILE;
+      const int row = row0 + lane, rows = min(32, p.m - row0);
+      // scales and biases, while the products run
+      const float sa = row < p.m ? p.sa[row] : 0.f;
+      float sw[4], bias[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = col0 + c0 + 32 * i + lane;
+        sw[i] = at < p.n ? p.sw[at] : 0.f;
+        bias[i] = biased && at < p.n ? p.bias[at] : 0.f;
+      }
       const bool ok = mbar_wait(&acc_full[b], (n >> 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) atomicOr(&tc::hadq_tc_fault, tc::kFaultEpilogue);
         break;
       }
       tc_fence_after();
-      const int row0 = im * C::TILE + rank * 128 + quarter * 32, col0 = in * C::TILE;
-      const int row = row0 + lane;
-      const float sa = row < p.m ? p.sa[row] : 0.f;
       const uint32_t taddr = tmem + b * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < C::TILE; c += 32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 32 * i;
         int v[32];
         tmem_ld32i(taddr + c, v);
         tmem_wait_ld();
-        if (c + 32 == C::TILE) {                                      // the last read: the MMAs may overwrite
+        if (i == 3) {                                                 // the last read: the MMAs may overwrite
           tc_fence_before();
           __syncwarp();
           if (lane == 0)
@@ -661,19 +692,21 @@ imm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         }
         const int col = col0 + c;
         if (col >= p.n) continue;
-        // Scales of the 32 columns: lane c's, passed around; rows turned so
-        // that a warp stores runs of columns (any n, any alignment).
-        const bool in_n = col + lane < p.n;
-        const float sw = in_n ? p.sw[col + lane] : 0.f;
-        const float bias = in_n && p.bias != nullptr ? p.bias[col + lane] : 0.f;
+        // Rows are turned through shared memory, so that a warp stores runs of
+        // columns (any n, any alignment); eight are read before the first is stored.
 #pragma unroll
         for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = scaled(v[j], sa);
         __syncwarp();
-        const int rows = min(32, p.m - row0);
-        for (int r = 0; r < rows; ++r) {
-          if (in_n)
-            store_one<OUT_BF16>(p.out, static_cast<int64_t>(row0 + r) * p.n + col + lane,
-                                finish(turn[r * 33 + lane], sw, p.bias != nullptr, bias));
+        int64_t e = static_cast<int64_t>(row0) * p.n + col + lane;
+        const bool in_n = col + lane < p.n;
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 8) {
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = finish(turn[(r + j) * 33 + lane], sw[i], biased, bias[i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j, e += p.n)
+            if (in_n && r + j < rows) store_one<OUT_BF16>(p.out, e, y[j]);
         }
         __syncwarp();
       }

@@ -124,13 +124,13 @@ using ImmSplitFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Arg
 using ImmPairFn = void (*)(const CUtensorMap, const CUtensorMap, const imm::Args);
 struct ImmSplitVariant {
   ImmSplitFn fn;
-  int threads, smem, tokens;
+  int threads, smem, tokens, ctas;           // ctas: on an SM
 };
 struct ImmPairVariant {
   ImmPairFn fn;
   int threads, smem;
 };
-ImmSplitVariant imm_split_for(int64_t m, bool out_bf16);
+ImmSplitVariant imm_split_for(int64_t m, bool many_tiles, bool out_bf16);
 ImmPairVariant imm_pair_for(bool out_bf16);
 int imm_fault_bits(int clear);
 

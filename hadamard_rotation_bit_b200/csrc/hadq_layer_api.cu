@@ -80,7 +80,7 @@ hadq_status int8_map(const int8_t* p, int64_t rows, int64_t k, int box_rows, CUt
   return r == CUDA_SUCCESS ? HADQ_OK : fail(HADQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
-hadq_status launch_imm(const hadq::imm::Args& p, bool out_bf16, cudaStream_t stream) {
+hadq_status launch_imm(hadq::imm::Args p, bool out_bf16, cudaStream_t stream) {
   if (p.m <= 4) {
     // k is divided among a CTA's warps until there are two CTAs to an SM, as
     // long as a warp has four rounds over it (1 x 4096 x 14336 undivided
@@ -111,9 +111,12 @@ hadq_status launch_imm(const hadq::imm::Args& p, bool out_bf16, cudaStream_t str
   CUtensorMap map_a, map_w;
   const int64_t pair_tiles = ceil_div(p.m, 256) * ceil_div(p.n, 256);
   // Many tokens: from 40 tiles of 256 x 256 on, half of the GPU's 74 pairs.
-  // 1024 x 4096 x 4096 (64 tiles) takes 22.0 us in pairs and 34.8 split,
-  // 512 x 4096 x 4096 (32 tiles) 21.6 and 17.9.
-  if (p.m > 128 && pair_tiles >= 40) {
+  // 768 x 4096 x 4096 (48 tiles) takes 17.7 us in pairs and 30.8 split, 512 x
+  // 4096 x 4096 (32 tiles) 16.7 and 16.3.  Up to 128 tokens half of a tile is
+  // empty, and pairs pay once the split kernel's tiles no longer fit the SMs at
+  // once: 96 x 28672 x 4096 (112 tiles) 30.9 and 34.1, 96 x 14336 x 4096 (56) 18.3
+  // and 17.6.
+  if (p.m > 128 ? pair_tiles >= 40 : p.m > 64 && pair_tiles > sms / 2) {
     const hl::ImmPairVariant v = hl::imm_pair_for(out_bf16);
     st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
     if (st == HADQ_OK) st = int8_map(p.a, p.m, p.k, 128, &map_a);
@@ -124,17 +127,27 @@ hadq_status launch_imm(const hadq::imm::Args& p, bool out_bf16, cudaStream_t str
     return launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(grid)), 2, v.threads, v.smem, stream, map_a, map_w, p),
                          "int8 matrix product launch");
   }
-  const hl::ImmSplitVariant v = hl::imm_split_for(p.m, out_bf16);
+  // Tiles that do not fit the SMs at once share them, two to an SM with half the
+  // ring each, where the rings are small enough: 48 x 28672 x 4096 22.9 us, 28.2
+  // with one; 48 x 14336 x 4096 fits, 13.7 with the whole ring and 15.7 with half.
+  const hl::ImmSplitVariant v = hl::imm_split_for(p.m, ceil_div(p.n, 128) > sms, out_bf16);
   st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
-  if (st == HADQ_OK) st = int8_map(p.a, p.m, p.k, v.tokens, &map_a);
+  const int64_t token_tiles = ceil_div(p.m, v.tokens);
+  p.tokens = static_cast<int>(ceil_div(ceil_div(p.m, token_tiles), 8) * 8);
+  if (st == HADQ_OK) st = int8_map(p.a, p.m, p.k, p.tokens, &map_a);
   if (st == HADQ_OK) st = int8_map(p.w, p.n, p.k, 128, &map_w);
   if (st != HADQ_OK) return st;
-  const int64_t token_tiles = ceil_div(p.m, v.tokens), tiles = ceil_div(p.n, 128) * token_tiles;
+  const int64_t tiles = ceil_div(p.n, 128) * token_tiles;
   const int64_t slices = ceil_div(p.k, hadq::imm::kSlice);
   // k is split as long as every CTA is resident at once (333 x 1001 x 4112: 13.5
-  // us with 48 CTAs, 10.0 with 96, 17.0 with 192) and has four slices.
+  // us with 48 CTAs, 10.0 with 96, 17.0 with 192) and has four slices, or eight
+  // where two CTAs share an SM (24 tokens, 4096 x 14336: 13.4 with 256 CTAs, 14.8
+  // with 128; 4096 x 4096: 7.2 and 6.9).
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= int64_t(sms) * occ && slices >= 8 * splits) splits *= 2;
+  for (; splits < 8; splits *= 2) {
+    const int64_t ctas = tiles * splits * 2;
+    if (ctas > int64_t(sms) * v.ctas || slices < (ctas <= sms ? 4 : 8) * 2 * splits) break;
+  }
   if (tiles * splits > INT32_MAX) return unsupported("too many output tiles");
   return launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(tiles * splits)), splits, v.threads, v.smem, stream, map_w,
                                    map_a, p, splits, static_cast<int>(token_tiles)),
@@ -305,7 +318,7 @@ hadq_status hadq_matmul_int8(const int8_t* a, const float* a_scales, int64_t row
     hadq_status st = disjoint(&o, 1, ins, 5, "out must not overlap an input");
     if (st != HADQ_OK) return st;
     const hadq::imm::Args p{a, w, a_scales, w_scales, bias, out, static_cast<int>(rows), static_cast<int>(cols),
-                            static_cast<int>(k)};
+                            static_cast<int>(k), 0};
     return launch_imm(p, out_dtype == HADQ_BF16, static_cast<cudaStream_t>(stream));
   });
 }
