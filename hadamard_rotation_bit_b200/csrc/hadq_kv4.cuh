@@ -8,6 +8,8 @@
 // one of scales (page_size is a multiple of 16): the tile of both kernels.
 #pragma once
 
+#include <climits>
+
 #include "hadq_device.cuh"
 
 namespace hadq {
@@ -216,6 +218,7 @@ struct AttnArgs {
   Divider row_tiles;
   Divider blocks;            // page_size / 16
   int units, splits;
+  int sorted;                // sequences, to be taken longest first; 0: as they come
   int rotate;
   float norm;                // fp32(1 / sqrt(D))
   float scale_log2;          // scale * log2(e)
@@ -381,8 +384,35 @@ __device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
   return n < 0 ? 0 : n > most ? most : n;
 }
 
+// The sequence whose turn is `turn` when runs of 64 sequences go in order of
+// their lengths, the longest first: more CTAs than the GPU holds then end with
+// short ones.  Two threads to a sequence count those before it; runs of 256,
+// eight times the counting, cost what they gained (300 sequences of about 750:
+// 109 us, in no order 77).
+__device__ __forceinline__ int by_length(const AttnArgs& a, int turn, int* lens) {
+  constexpr int kRun = 16 * kWarps;
+  __shared__ int chosen;
+  const int first = turn & ~(kRun - 1), n = min(kRun, a.sorted - first);
+  if (threadIdx.x < kRun) lens[threadIdx.x] = threadIdx.x < n ? a.lengths[first + threadIdx.x] : INT_MIN;
+  __syncthreads();
+  const int s = threadIdx.x >> 1, half = threadIdx.x & 1, mine = lens[s];
+  int before = 0;
+#pragma unroll
+  for (int j = 0; j < kRun / 2; j += 4) {       // (length, place) is an order of all of them
+    const int i = half * (kRun / 2) + j;
+    const int4 x = *reinterpret_cast<const int4*>(lens + i);
+    before += (x.x > mine || (x.x == mine && i < s)) + (x.y > mine || (x.y == mine && i + 1 < s)) +
+              (x.z > mine || (x.z == mine && i + 2 < s)) + (x.w > mine || (x.w == mine && i + 3 < s));
+  }
+  before += __shfl_xor_sync(0xffffffffu, before, 1);
+  if (before == turn - first && s < n) chosen = first + s;
+  __syncthreads();                              // and `lens` is free again
+  return chosen;
+}
+
 // Division of the work.  A unit is a (sequence, K/V head, tile of query rows);
-// CTA (unit, split) takes the split's equal part of the sequence's steps.  With
+// CTA (unit, split) takes the split's equal part of the sequence's steps, the
+// longest sequences first where that shortens the grid's end (longest_first).  With
 // more than one split the parts' sums go to the workspace, and kv4_join_kernel
 // adds them in order.
 template <int D, int GROUP, int NT, int STAGES>
@@ -401,9 +431,12 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) kv4_attention_ke
 
   grid_dependency_sync();
   const int ratio = a.ratio.d, rows = a.q_len * ratio;
-  const int unit = blockIdx.x, split = blockIdx.y;
-  const int bh = static_cast<int>(a.row_tiles(unit)), rt = unit - bh * a.row_tiles.d;
-  const int b = static_cast<int>(a.kv_heads(bh)), h = bh - b * a.kv_heads.d;
+  const int split = blockIdx.y;
+  const int turn = static_cast<int>(a.row_tiles(blockIdx.x)), rt = blockIdx.x - turn * a.row_tiles.d;
+  int b = static_cast<int>(a.kv_heads(turn));
+  const int h = turn - b * a.kv_heads.d;
+  if (a.sorted > 0) b = by_length(a, b, reinterpret_cast<int*>(smem));
+  const int unit = (b * a.kv_heads.d + h) * a.row_tiles.d + rt;
   // the query's values, on their way while the length and the page table are read
   constexpr int LPR = D / 8, PASS = kWarps * 32 / LPR;        // lanes per row, rows of a pass of all warps
   constexpr int PASSES = (C::ROWS + PASS - 1) / PASS;

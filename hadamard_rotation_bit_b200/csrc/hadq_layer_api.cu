@@ -232,6 +232,18 @@ int attention_splits(const hl::AttnVariant& v, int64_t units, int64_t max_positi
   return static_cast<int>(std::max<int64_t>(1, std::min(want, steps / 4)));
 }
 
+// Sequences by length where the grid's end would otherwise wait for a long one:
+// more CTAs than fit at once, but no more than three times as many, of 1024
+// positions or more.  (Device us in this order and as they come: 64 sequences of
+// 0 to 6000 positions, 512 CTAs of 296 places, 76.6 and 103; of 1792 to 3584, 73.4
+// and 82.7; all of 3584, 97.5 and 97.3; 1024 CTAs of 592 places, 118 and 126, equal
+// lengths 145 and 144.  What the counting costs shows with many or short CTAs: 3200
+// of 296 places 103 and 99, 2048 of 592 with 256 positions 32.4 and 30.4.)
+bool longest_first(const hl::AttnVariant& v, int64_t ctas, int64_t positions) {
+  const int64_t slots = 148 * v.ctas;
+  return ctas > slots && ctas <= 3 * slots && positions >= 1024;
+}
+
 int64_t attention_units(const hl::AttnVariant& v, int64_t batch, int64_t rows, int64_t kv_heads) {
   return batch * kv_heads * ceil_div(rows, v.rows);
 }
@@ -453,6 +465,7 @@ hadq_status hadq_kv4_attention(const void* q, int64_t q_stride, hadq_dtype dtype
     p.blocks = divider(static_cast<uint32_t>(page_size / 16));
     p.units = static_cast<int>(units);
     p.splits = splits;
+    p.sorted = longest_first(v, units * splits, max_pages * page_size / splits) ? static_cast<int>(batch) : 0;
     p.rotate = rotate;
     p.norm = static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);

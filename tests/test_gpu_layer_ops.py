@@ -481,6 +481,21 @@ def test_attention_bad_pages_and_lengths_are_recorded():
     assert not bool(out[0].any()) and torch.equal(out[2], want[2])
 
 
+@pytest.mark.parametrize("batch,q_len,kv_heads,ratio", [(75, 2, 8, 8), (150, 1, 8, 1), (64, 3, 6, 4), (65, 1, 16, 2)])
+def test_attention_batches_beyond_the_gpu(batch, q_len, kv_heads, ratio):
+    """More units than are computed at once, lengths of all sizes, equal ones and empty ones among them."""
+    g = torch.Generator().manual_seed(batch)
+    lengths = torch.randint(0, 1101, (batch,), generator=g).tolist()
+    lengths[3], lengths[5], lengths[-1], lengths[-2], lengths[7] = 0, 1100, 1100, 0, lengths[8]
+    q, cache, table, ln = attention_case(18, batch, q_len, kv_heads, ratio, 128, 128, 64, lengths)
+    out = H.hadq_kv4_attention(q, *cache, table, ln)
+    check_attention(out, q, cache, table, ln, 128 ** -0.5, True)
+    # the same sequences in another order
+    order = torch.randperm(batch, generator=g).cuda()
+    again = H.hadq_kv4_attention(q[order].contiguous(), *cache, table[order].contiguous(), ln[order].contiguous())
+    assert torch.equal(again, out[order])
+
+
 @pytest.mark.parametrize("as_handle", [False, True])
 def test_attention_on_another_stream_keeps_its_workspace(as_handle):
     """Memory that this stream asks for after the call is not what the other stream still computes in."""
