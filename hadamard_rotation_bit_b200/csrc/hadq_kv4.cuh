@@ -97,7 +97,7 @@ __device__ __forceinline__ void load32(const void* x, int64_t e, float (&v)[32])
 }
 
 // Even CTAs store K, odd ones V, side by side: one computes, the other copies.
-// Five CTAs an SM hide the loads (32768 tokens x 8 heads x 128: 38.3 us, 4.4
+// Five CTAs an SM hide the loads (32768 tokens x 8 heads x 128: 38.0 us, 4.4
 // TB/s; 41 with four, 43.3 with resident CTAs that load ahead into registers).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256, 5) kv4_append_kernel(const __grid_constant__ AppendArgs a) {
@@ -187,9 +187,11 @@ __global__ void __launch_bounds__(256, 5) kv4_append_kernel(const __grid_constan
 // each warp in a ring of its own: the loop has no block-wide barrier.
 //
 // Measured (device time): 16 sequences x 32 heads x 3584 .. 4096 positions, 128
-// wide, one scale per row: 53.6 us, 4.87 TB/s of codes and scales.  The fp16
-// form of K's products took 60.5 us, one tile a step 73, V's 8 taken off by
-// products of its own 65, 24 warps instead of 16 (fewer registers) 64.
+// wide, one scale per row: 56 us, 4.65 TB/s of codes and scales.  When it took
+// 53.6 (a tile of rows had one unit, sequences no order), the fp16 form of K's
+// products took 60.5 us, one tile a step 73, V's 8 taken off by products of its
+// own 65, 24 warps instead of 16 (fewer registers) 64.  With its copies taken out
+// the loop still takes 49: it is bound by issue, not by memory.
 //
 // Rounding: q to 2^-15 of its row's largest value (digits) or to fp16, P to
 // fp16 (2^-11 relative; the running maximum bounds it by 2^8).  Codes are exact,
