@@ -130,7 +130,7 @@ struct ImmPairVariant {
   ImmPairFn fn;
   int threads, smem;
 };
-ImmSplitVariant imm_split_for(int64_t m, bool many_tiles, bool out_bf16);
+ImmSplitVariant imm_split_for(int64_t m, bool half, bool out_bf16);
 ImmPairVariant imm_pair_for(bool out_bf16);
 int imm_fault_bits(int clear);
 

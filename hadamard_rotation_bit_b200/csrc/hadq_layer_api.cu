@@ -130,7 +130,15 @@ hadq_status launch_imm(hadq::imm::Args p, bool out_bf16, cudaStream_t stream) {
   // Tiles that do not fit the SMs at once share them, two to an SM with half the
   // ring each, where the rings are small enough: 48 x 28672 x 4096 22.9 us, 28.2
   // with one; 48 x 14336 x 4096 fits, 13.7 with the whole ring and 15.7 with half.
-  const hl::ImmSplitVariant v = hl::imm_split_for(p.m, ceil_div(p.n, 128) > sms, out_bf16);
+  // Above 64 tokens such tiles of 64 tokens also beat those of 128, whose joins and
+  // epilogues are longer, until reading the weights again outweighs it, at about 14
+  // slices of a 128 x 128 tile an SM: 128 x 2048 x 4096 (512 slices) 7.5 and 8.5 us,
+  // 96 x 6144 x 4096 (1536) 12.2 and 13.1, 256 x 4096 x 4096 (2048) 12.9 and 13.0,
+  // 333 x 4096 x 4096 (3072) 16.0 and 15.3, 200 x 8192 x 8192 (8192) 27.9 and 25.7;
+  // against the rule 333 x 1001 x 4112 (792) 10.1 and 9.6.
+  const int64_t work = ceil_div(p.m, 128) * ceil_div(p.n, 128) * ceil_div(p.k, hadq::imm::kSlice);
+  const bool half = p.m > 64 ? work < 14 * sms : ceil_div(p.n, 128) > sms;
+  const hl::ImmSplitVariant v = hl::imm_split_for(p.m, half, out_bf16);
   st = occupancy(reinterpret_cast<const void*>(v.fn), dev, v.threads, v.smem, &occ);
   const int64_t token_tiles = ceil_div(p.m, v.tokens);
   p.tokens = static_cast<int>(ceil_div(ceil_div(p.m, token_tiles), 8) * 8);
@@ -140,13 +148,16 @@ hadq_status launch_imm(hadq::imm::Args p, bool out_bf16, cudaStream_t stream) {
   const int64_t tiles = ceil_div(p.n, 128) * token_tiles;
   const int64_t slices = ceil_div(p.k, hadq::imm::kSlice);
   // k is split as long as every CTA is resident at once (333 x 1001 x 4112: 13.5
-  // us with 48 CTAs, 10.0 with 96, 17.0 with 192) and has four slices, or eight
+  // us with 48 CTAs, 10.0 with 96, 17.0 with 192; 48 x 2048 x 4096: 6.5 with 64,
+  // 10.3 with 128 in clusters of 8, of which 15 fit) and has four slices, or eight
   // where two CTAs share an SM (24 tokens, 4096 x 14336: 13.4 with 256 CTAs, 14.8
   // with 128; 4096 x 4096: 7.2 and 6.9).
   int splits = 1;
   for (; splits < 8; splits *= 2) {
     const int64_t ctas = tiles * splits * 2;
-    if (ctas > int64_t(sms) * v.ctas || slices < (ctas <= sms ? 4 : 8) * 2 * splits) break;
+    // what fits at once (of 148 SMs): clusters of 4 and 8 leave some SMs of a GPC without a CTA
+    const int lost = splits == 4 ? (v.ctas > 1 ? 16 : 28) : splits == 2 ? (v.ctas > 1 ? 6 : 16) : 0;
+    if (ctas > int64_t(sms - lost) * v.ctas || slices < (ctas <= sms ? 4 : 8) * 2 * splits) break;
   }
   if (tiles * splits > INT32_MAX) return unsupported("too many output tiles");
   return launch_result(launch_pdl3(v.fn, dim3(static_cast<unsigned>(tiles * splits)), splits, v.threads, v.smem, stream, map_w,

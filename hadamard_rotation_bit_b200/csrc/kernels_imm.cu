@@ -36,9 +36,10 @@ ImmWarpVariant imm_warp_for(int64_t m, bool two, bool out_bf16) {
   return two ? warp_variant<2>(m, out_bf16) : warp_variant<1>(m, out_bf16);
 }
 
-ImmSplitVariant imm_split_for(int64_t m, bool many_tiles, bool out_bf16) {
+ImmSplitVariant imm_split_for(int64_t m, bool half, bool out_bf16) {
   if (m <= 32) return split<32, 4>(out_bf16);
-  if (m <= 64) return many_tiles ? split<64, 3>(out_bf16) : split<64, 6>(out_bf16);
+  if (half) return split<64, 3>(out_bf16);
+  if (m <= 64) return split<64, 6>(out_bf16);
   return split<128, 4>(out_bf16);
 }
 

@@ -173,7 +173,8 @@ def check_matmul(out, a, sa, w, sw, bias):
                                    (333, 1001, 4112), (512, 4096, 1024), (1025, 520, 384), (2000, 24, 256),
                                    (40, 20000, 64), (300, 8, 16), (1300, 2100, 208), (300, 5201, 4112), (200, 10250, 64),
                                    (10300, 40, 96), (2048, 2048, 1024), (2817, 1032, 272),
-                                   (70, 19201, 80), (128, 20000, 144), (64, 19300, 272), (50, 19000, 1040), (20, 4100, 8192), (65, 129, 4096)])
+                                   (70, 19201, 80), (128, 20000, 144), (64, 19300, 272), (50, 19000, 1040), (20, 4100, 8192), (65, 129, 4096),
+                                   (90, 8200, 8192), (200, 2047, 14336), (333, 4100, 4112), (130, 500, 65536), (200, 6101, 4112)])
 def test_matmul(m, n, k, out):
     g = gen(m + n + k)
     a = torch.randint(-127, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
