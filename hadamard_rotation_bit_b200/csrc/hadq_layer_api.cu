@@ -134,7 +134,7 @@ hadq_status launch_imm(hadq::imm::Args p, bool out_bf16, cudaStream_t stream) {
   // epilogues are longer, until reading the weights again outweighs it, at about 14
   // slices of a 128 x 128 tile an SM: 128 x 2048 x 4096 (512 slices) 7.5 and 8.5 us,
   // 96 x 6144 x 4096 (1536) 12.2 and 13.1, 256 x 4096 x 4096 (2048) 12.9 and 13.0,
-  // 333 x 4096 x 4096 (3072) 16.0 and 15.3, 200 x 8192 x 8192 (8192) 27.9 and 25.7;
+  // 333 x 4096 x 4096 (half as much again) 16.0 and 15.3, 200 x 8192 x 8192 (8192) 27.9 and 25.7;
   // against the rule 333 x 1001 x 4112 (792) 10.1 and 9.6.
   const int64_t work = ceil_div(p.m, 128) * ceil_div(p.n, 128) * ceil_div(p.k, hadq::imm::kSlice);
   const bool half = p.m > 64 ? work < 14 * sms : ceil_div(p.n, 128) > sms;
